@@ -13,7 +13,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
-ABI_VERSION = 9
+ABI_VERSION = 10
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 GATE_SCALAR, GATE_PER_KEY = 0, 1
@@ -27,7 +27,11 @@ EXPORTS = sorted(["gdn_abi_version", "gdn_status_str", "gdn_last_error",
                   "gdn_chunk_fwd_act", "gdn_recurrent_step_act",
                   "gdn_chunk_bwd_workspace", "gdn_chunk_bwd", "gdn_chunk_bwd_act",
                   "gdn_seqlens_status_offset", "gdn_sync_status_offset",
-                  "gdn_chunk_fwd_noalloc"])
+                  "gdn_chunk_fwd_noalloc",
+                  "gdn_linrec_workspace", "gdn_linrec_fwd", "gdn_linrec_bwd", "gdn_linrec_step",
+                  "gdn_qk_norm_rope", "gdn_qk_norm_rope_bwd_workspace", "gdn_qk_norm_rope_bwd",
+                  "gdn_short_conv_workspace", "gdn_short_conv_fwd", "gdn_short_conv_bwd",
+                  "gdn_short_conv_step"])
 INTRA_STORE_AINV = 1
 ACT_GATE, ACT_BETA_SIGMOID, ACT_BETA_NEG_EIG, ACT_QK_L2NORM = 1, 2, 4, 8
 
@@ -123,6 +127,8 @@ def load(path: str = LIB_PATH):
     v = lib.gdn_abi_version()
     if v != ABI_VERSION:
         raise RuntimeError("libgdn.so ABI %d, binding expects %d" % (v, ABI_VERSION))
+    from . import _layer
+    _layer.declare(lib)
     _lib = lib
     return lib
 

@@ -11,6 +11,7 @@
 
 #include "../../include/gdn.h"
 #include "gdn_launch.hpp"
+#include "gdn_layer.hpp"
 
 namespace {
 
@@ -321,6 +322,17 @@ gdn_status scratch_of_current_device(void** out) {
 }
 
 }  // namespace
+
+namespace gdn {
+gdn_status api_fail(gdn_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+gdn_status api_ok() { return ok(); }
+}  // namespace gdn
 
 extern "C" {
 

@@ -1,0 +1,124 @@
+// Internal launcher interface of the layer operators (gated linear
+// recurrence, q/k norm with rotation, short convolution) between
+// gdn_layer_api.hip and their kernel translation units, and the device
+// helpers these share.  Not part of the public ABI.
+#pragma once
+
+#include "../../include/gdn.h"
+#include "gdn_device.hpp"
+#include "gdn_launch.hpp"
+
+namespace gdn {
+
+// error reporting of the C ABI (gdn_api.hip): the status, with its detail
+// left for gdn_last_error()
+gdn_status api_fail(gdn_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+gdn_status api_ok();
+
+// Tiles of `tile` tokens that never cross a sequence.  Without packed offsets
+// tile c is tokens (c % nt) * tile .. of sequence c / nt; with them a table
+// built on the device gives (first token, count, sequence, tile of its
+// sequence), count 0 for unused rows.
+struct SeqMap {
+    const int4* table = nullptr;   // [max_tiles] or nullptr
+    const int4* seqs = nullptr;    // [N] (first token, length, first tile, 0) or nullptr
+    int64_t T = 0;                 // tokens per sequence when table == nullptr
+    int64_t nt = 0;                // tiles per sequence when table == nullptr
+    int64_t N = 0;
+    int64_t max_tiles = 0;
+    int tile = 0;
+};
+
+struct Tile {
+    int64_t row0;   // first token (row of the activations)
+    int n;          // tokens; 0: unused
+    int seq;
+    int j;          // tile of its sequence
+    int last;       // 1: the sequence's last tile
+};
+
+__device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
+    Tile t;
+    if (m.table) {
+        const int4 r = m.table[c];
+        t.row0 = r.x;
+        t.n = r.y;
+        t.seq = r.z;
+        t.j = r.w;
+        t.last = 0;
+        if (r.y > 0) t.last = (int64_t)(r.w + 1) * m.tile >= m.seqs[r.z].y;
+    } else {
+        const int64_t b = c / m.nt;
+        t.j = (int)(c - b * m.nt);
+        t.seq = (int)b;
+        const int64_t at = (int64_t)t.j * m.tile;
+        t.row0 = b * m.T + at;
+        t.n = (int)min((int64_t)m.tile, m.T - at);
+        t.last = t.j == m.nt - 1;
+    }
+    return t;
+}
+
+// Packed offsets to the table of SeqMap; words[0] = the check of the offsets.
+struct TileTableLaunch {
+    const int64_t* cu_seqlens;
+    int64_t N, T, max_tiles;
+    int tile;
+    int4 *table, *seqs;
+    int* words;
+    hipStream_t stream;
+};
+hipError_t launch_tile_table(const TileTableLaunch& a);
+
+struct LinrecLaunch {
+    SeqMap map;
+    Act act;                      // ACT_GATE: A_log, dt_bias [D]
+    bool normalize = false;
+    const void *x = nullptr, *g = nullptr, *dy = nullptr;
+    const float *h0 = nullptr, *dht = nullptr;
+    void *y = nullptr, *dx = nullptr, *dg = nullptr;
+    float *ht = nullptr, *dh0 = nullptr, *dA_log = nullptr, *ddt_bias = nullptr;
+    float* states = nullptr;
+    float* hbuf = nullptr;        // [B*T][D] states of every token (backward)
+    float* part = nullptr;        // [N][2][D] sums of dA_log and ddt_bias (backward)
+    int64_t D = 0, xs = 0, gs = 0, ys = 0;   // channels; token strides of x, g, y / dy
+    bool x_bf16 = false, g_bf16 = false;
+    hipStream_t stream = nullptr;
+};
+hipError_t launch_linrec_fwd(const LinrecLaunch& a);
+hipError_t launch_linrec_bwd(const LinrecLaunch& a);
+hipError_t launch_linrec_step(const LinrecLaunch& a);
+
+struct QkLaunch {
+    const void *q, *k;
+    const float *qw, *kw;
+    const double* inv_freq;
+    const int64_t* positions;
+    void *qo, *ko;                // forward: outputs; backward: dq, dk
+    const void *dqo = nullptr, *dko = nullptr;
+    float *dqw = nullptr, *dkw = nullptr, *part = nullptr;
+    int64_t tokens, T, Hq, Hk, qs, ks, qhs, khs;
+    int D, R, norm;
+    bool interleaved, bf16;
+    float eps, offset;
+    hipStream_t stream;
+};
+hipError_t launch_qk(const QkLaunch& a);
+hipError_t launch_qk_bwd(const QkLaunch& a);
+
+struct ConvLaunch {
+    SeqMap map;
+    const void *x = nullptr, *s0 = nullptr, *dy = nullptr, *dst = nullptr;
+    const float *w = nullptr, *b = nullptr;
+    void *y = nullptr, *st = nullptr, *dx = nullptr, *ds0 = nullptr;
+    float *dw = nullptr, *db = nullptr, *part = nullptr;
+    int64_t D = 0, xs = 0, ys = 0;
+    int W = 0;
+    bool silu = false, bf16 = false;
+    hipStream_t stream = nullptr;
+};
+hipError_t launch_conv_fwd(const ConvLaunch& a);
+hipError_t launch_conv_bwd(const ConvLaunch& a);
+hipError_t launch_conv_step(const ConvLaunch& a);
+
+}  // namespace gdn

@@ -1,6 +1,9 @@
 /*
  * gdn.h -- C ABI of the MI355X (gfx950) gated delta rule library: the
- * chunked forward, the single-token decode step and the chunked backward.
+ * chunked forward, the single-token decode step and the chunked backward;
+ * and the operators a layer puts around them: the gated linear recurrence
+ * (gdn_linrec_*), the per-head norm of q and k with the position rotation
+ * (gdn_qk_norm_rope*) and the short causal convolution (gdn_short_conv_*).
  *
  * The operation (the "gated delta rule"):
  *
@@ -50,7 +53,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 9
+#define GDN_ABI_VERSION 10
 
 typedef int32_t gdn_status;
 enum {
@@ -473,6 +476,195 @@ gdn_status gdn_chunk_bwd_act(const gdn_fwd_desc *d, const gdn_activation *act,
                              void *dq, void *dk, void *dv, float *dbeta, float *dg, float *dh0,
                              float *dA_log, float *ddt_bias,
                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* ======================================================================
+ * Layer operators.  The conventions at the top hold, with these additions:
+ *  - Activations may be rows of a wider tensor: a *_stride member gives the
+ *    elements between consecutive tokens (0: dense rows).  Token t of
+ *    sequence b is row b * seq_len + t of that spacing.
+ *  - A packed call's check of cu_seqlens (0: offsets start at 0, never
+ *    decrease and end at seq_len; 1: not) is the first int32 of its
+ *    workspace once the stream has reached the call.  Offsets are clamped
+ *    into [0, seq_len] as above.
+ *  - Calls that may overlap need workspaces of their own.
+ * ====================================================================== */
+
+/*
+ * Gated linear recurrence over D channels:
+ *   h_t = a_t h_{t-1} + u_t ,  y_t = h_t ,  a_t = exp(g_t),
+ *   u_t = x_t, or sqrt(1 - a_t^2) x_t with GDN_LINREC_NORMALIZE (g <= 0 then).
+ * With act (flags GDN_ACT_GATE or 0; other flags give GDN_ERR_UNSUPPORTED) g
+ * holds raw logits and log a = -exp(A_log[c]) softplus(g + dt_bias[c]), A_log
+ * and dt_bias [D] float.  The state is kept in fp32.
+ */
+enum { GDN_LINREC_NORMALIZE = 1 };
+typedef struct gdn_linrec_desc {
+    int64_t batch;      /* B; must be 1 when cu_seqlens is given */
+    int64_t seq_len;    /* T: tokens per sequence, or all packed tokens */
+    int64_t channels;   /* D >= 1 */
+    int64_t num_seqs;   /* N packed sequences when cu_seqlens is given, else 0 */
+    int64_t x_stride;   /* token strides of x, of g and of y / dy */
+    int64_t g_stride;
+    int64_t y_stride;
+    int32_t x_dtype;    /* GDN_DTYPE_* of x, y, dy, dx */
+    int32_t g_dtype;    /* GDN_DTYPE_* of g, dg */
+    int32_t flags;      /* GDN_LINREC_* */
+} gdn_linrec_desc;
+
+/*
+ * Bytes of workspace of gdn_linrec_fwd (backward = 0) or gdn_linrec_bwd
+ * (backward = 1) for *d (num_seqs > 0: packed), and the rows of its `states`
+ * argument.  Either output may be NULL.  0 bytes: no workspace is needed.
+ */
+gdn_status gdn_linrec_workspace(const gdn_linrec_desc *d, int32_t backward, size_t *bytes,
+                                int64_t *state_rows);
+
+/*
+ *   x       [B, T, D]  x_dtype          g   [B, T, D]  g_dtype
+ *   h0      [N, D] float, initial state, NULL: zeros
+ *   y       [B, T, D]  x_dtype, output; NULL: not computed
+ *   ht      [N, D] float, final state (h0 of an empty sequence); NULL: not
+ *           returned.  ht may equal h0.
+ *   states  [state_rows, D] float, NULL: not kept.  States at the borders of
+ *           the kernel's tiles, for a gdn_linrec_bwd of the same descriptor
+ *           and inputs.
+ * N = B without cu_seqlens, num_seqs with it.
+ */
+gdn_status gdn_linrec_fwd(const gdn_linrec_desc *d, const gdn_activation *act,
+                          const void *x, const void *g, const float *h0,
+                          const int64_t *cu_seqlens, void *y, float *ht, float *states,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of <dy, y> + <dht, ht>.  With dh_t the gradient of h_t:
+ *   dh_t = dy_t + a_{t+1} dh_{t+1} (dh of a last token also takes dht),
+ *   dx_t = dh_t (times m_t = sqrt(1 - a_t^2) with GDN_LINREC_NORMALIZE),
+ *   dlog a_t = dh_t (a_t h_{t-1} - x_t a_t^2 / m_t), the second term with
+ *   GDN_LINREC_NORMALIZE only and 0 where m_t = 0.
+ *   dy      [B, T, D] x_dtype (stride y_stride);  dht [N, D] float or NULL
+ *   states  what gdn_linrec_fwd left for the same inputs, or NULL: recomputed
+ *   dx [B, T, D] x_dtype, dg [B, T, D] g_dtype, written, dense rows
+ *   dh0     [N, D] float, written, or NULL
+ *   dA_log, ddt_bias [D] float, written with GDN_ACT_GATE (required then)
+ * No output may alias an input or another output.  Sums over tokens are taken
+ * in a fixed order: the same call gives the same bits.
+ */
+gdn_status gdn_linrec_bwd(const gdn_linrec_desc *d, const gdn_activation *act,
+                          const void *x, const void *g, const float *h0,
+                          const int64_t *cu_seqlens, const void *dy, const float *dht,
+                          const float *states, void *dx, void *dg, float *dh0,
+                          float *dA_log, float *ddt_bias,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of batch sequences (seq_len must be 1, num_seqs 0; batch may be
+ * 0): state [B, D] float is updated in place, y [B, D] = the new state.
+ */
+gdn_status gdn_linrec_step(const gdn_linrec_desc *d, const gdn_activation *act,
+                           const void *x, const void *g, float *state, void *y, void *stream);
+
+/*
+ * Norm of every q and k head, then the rotation of its first R elements by
+ * position x inverse frequency, in one pass:
+ *   n = x r w,  r = 1 (GDN_NORM_NONE), 1 / sqrt(sum x^2 + eps) (GDN_NORM_L2) or
+ *               1 / sqrt(mean x^2 + eps) (GDN_NORM_RMS);
+ *               w = weight + weight_offset, 1 without a weight
+ *   (a', b') = (a cos t - b sin t, b cos t + a sin t),  t = position inv_freq[i],
+ * for the pairs (a, b) = (n[i], n[i + R/2]), or (n[2i], n[2i + 1]) with
+ * GDN_QK_INTERLEAVED, i < R/2; elements from R on are not rotated.  The angle
+ * is formed and reduced in 64 bits, so far positions lose nothing.
+ */
+enum { GDN_NORM_NONE = 0, GDN_NORM_L2 = 1, GDN_NORM_RMS = 2 };
+enum { GDN_QK_INTERLEAVED = 1 };
+typedef struct gdn_qk_desc {
+    int64_t batch;          /* B */
+    int64_t seq_len;        /* T; B*T tokens, packed or not */
+    int64_t q_heads;        /* >= 1 */
+    int64_t k_heads;        /* >= 1; independent of q_heads */
+    int64_t head_dim;       /* D: a multiple of 8 up to 256 */
+    int64_t rot_dim;        /* R: a multiple of 16 up to D; 0: no rotation */
+    int64_t q_stride;       /* token strides of the inputs q, k (0: heads x head stride) */
+    int64_t k_stride;
+    int64_t q_head_stride;  /* elements between heads of the inputs (0: D) */
+    int64_t k_head_stride;
+    int32_t dtype;          /* GDN_DTYPE_* of q, k and the outputs */
+    int32_t norm;           /* GDN_NORM_* */
+    int32_t flags;          /* GDN_QK_* */
+    float eps;
+    float weight_offset;
+} gdn_qk_desc;
+
+/*
+ *   q [B, T, Hq, D], k [B, T, Hk, D], strided as described; 16-byte aligned,
+ *     strides multiples of 8 elements
+ *   q_weight, k_weight  [D] float, each may be NULL
+ *   inv_freq   [R/2] double; positions [B, T] int64, any value (NULL: token t
+ *     of its row is at t); both ignored with R = 0
+ *   q_out, k_out  dense [B, T, Hq, D], [B, T, Hk, D], written
+ */
+gdn_status gdn_qk_norm_rope(const gdn_qk_desc *d, const void *q, const void *k,
+                            const float *q_weight, const float *k_weight,
+                            const double *inv_freq, const int64_t *positions,
+                            void *q_out, void *k_out, void *stream);
+
+/*
+ * Its gradients: dq_out, dk_out dense, 16-byte aligned; dq, dk dense, written;
+ * dq_weight, dk_weight [D] float, written, each may be NULL (and must be where
+ * the weight is).  Summed in a fixed order.  The workspace is 256-byte aligned.
+ */
+gdn_status gdn_qk_norm_rope_bwd_workspace(const gdn_qk_desc *d, size_t *bytes);
+gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_desc *d, const void *q, const void *k,
+                                const float *q_weight, const float *k_weight,
+                                const double *inv_freq, const int64_t *positions,
+                                const void *dq_out, const void *dk_out, void *dq, void *dk,
+                                float *dq_weight, float *dk_weight,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Short causal depthwise convolution, width W in 2..4:
+ *   z_t[c] = bias[c] + sum_j weight[c][j] x_{t-W+1+j}[c],
+ *   y = z, or z sigmoid(z) with GDN_CONV_SILU.
+ * Inputs before a sequence's first token come from its carried window s0
+ * (zeros without one).
+ */
+enum { GDN_CONV_SILU = 1 };
+typedef struct gdn_conv_desc {
+    int64_t batch, seq_len, channels, num_seqs;   /* as in gdn_linrec_desc */
+    int64_t x_stride;   /* token stride of x */
+    int64_t y_stride;   /* token stride of y / dy */
+    int32_t dtype;      /* GDN_DTYPE_* of x, y, s0, st and their gradients */
+    int32_t width;      /* W */
+    int32_t flags;      /* GDN_CONV_* */
+} gdn_conv_desc;
+
+gdn_status gdn_short_conv_workspace(const gdn_conv_desc *d, int32_t backward, size_t *bytes);
+
+/*
+ *   x [B, T, D], y [B, T, D] dtype;  weight [D, W], bias [D] float (bias may be NULL)
+ *   s0  [N, W-1, D] dtype, the inputs before each sequence, oldest first; NULL: zeros
+ *   st  [N, W-1, D] dtype, the last W-1 inputs (of s0 where the sequence is
+ *       shorter), written; NULL: not returned.  Must not overlap s0.
+ */
+gdn_status gdn_short_conv_fwd(const gdn_conv_desc *d, const void *x, const float *weight,
+                              const float *bias, const void *s0, const int64_t *cu_seqlens,
+                              void *y, void *st, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * Gradients of <dy, y> + <dst, st>: dx [B, T, D] dense, ds0 [N, W-1, D] (NULL:
+ * not computed), dweight [D, W] and dbias [D] float (dbias NULL iff bias is),
+ * all written, the sums over tokens in a fixed order.  dst may be NULL.
+ */
+gdn_status gdn_short_conv_bwd(const gdn_conv_desc *d, const void *x, const float *weight,
+                              const float *bias, const void *s0, const int64_t *cu_seqlens,
+                              const void *dy, const void *dst, void *dx, float *dweight,
+                              float *dbias, void *ds0,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of batch sequences (seq_len 1, num_seqs 0): the window state
+ * [B, W-1, D] moves on by x in place. */
+gdn_status gdn_short_conv_step(const gdn_conv_desc *d, const void *x, const float *weight,
+                               const float *bias, void *state, void *y, void *stream);
 
 #ifdef __cplusplus
 }
