@@ -128,17 +128,15 @@ def _workspace(ws, nbytes, dev):
     return ws, ws.numel() * ws.element_size()
 
 
-def _words(ws, dev, stream, packed):
-    """With GDN_DEBUG set: raise on the check of the offsets and on a wait that gave up."""
-    if ws is None or not _debug():
+def _words(ws, dev, stream, packed, waits=False):
+    """With GDN_DEBUG set: raise on the check of the offsets (packed) and on a wait that gave up."""
+    if ws is None or not (packed or waits) or not _debug():
         return
     (stream or torch.cuda.current_stream(dev)).synchronize()
     bad, wait = ws.view(torch.uint8)[:8].view(torch.int32).cpu().tolist()
-    if not packed:
-        return
-    if bad:
+    if packed and bad:
         raise GdnError(8, "cu_seqlens must start at 0, never decrease and end at T")
-    if wait:
+    if waits and wait:
         raise GdnError(7, "a wait between workgroups gave up: wrong results")
 
 
@@ -215,7 +213,7 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_b
     ht = ht if output_final_state else None
     _run(lib.gdn_linrec_fwd, dev, stream, d, act, _p(x), _p(g), _p(h0), _p(cu_seqlens), _p(y), _p(ht),
          _p(states), _p(workspace), have)
-    _words(workspace, dev, stream, cu_seqlens is not None)
+    _words(workspace, dev, stream, cu_seqlens is not None, rows > N)
     return y, ht
 
 
@@ -238,7 +236,7 @@ def linrec_bwd(x, g, dy, h0=None, dht=None, cu_seqlens=None, normalize=False, A_
     _f32c(h0, "h0", (N, D), dev)
     _f32c(dht, "dht", (N, D), dev)
     _f32c(states, "states", (_linrec_sizes(d, 0)[1], D), dev)
-    nbytes, _ = _linrec_sizes(d, 1)
+    nbytes, rows = _linrec_sizes(d, 1)
     out = dict(out or {})
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
         _out(out, "dx", x.shape, x.dtype, dev)
@@ -254,7 +252,7 @@ def linrec_bwd(x, g, dy, h0=None, dht=None, cu_seqlens=None, normalize=False, A_
     _run(lib.gdn_linrec_bwd, dev, stream, d, act, _p(x), _p(g), _p(h0), _p(cu_seqlens), _p(dy), _p(dht),
          _p(states), _p(out["dx"]), _p(out["dg"]), _p(out["dh0"]), _p(out.get("dA_log")) if act else None,
          _p(out.get("ddt_bias")) if act else None, _p(workspace), have)
-    _words(workspace, dev, stream, cu_seqlens is not None)
+    _words(workspace, dev, stream, cu_seqlens is not None, rows > N)
     return out
 
 
@@ -410,8 +408,7 @@ def short_conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, silu=True, ou
     st = st if output_final_state else None
     _run(lib.gdn_short_conv_fwd, dev, stream, d, _p(x), _p(weight), _p(bias), _p(s0), _p(cu_seqlens), _p(y),
          _p(st), _p(workspace), have)
-    if cu_seqlens is not None:
-        _words(workspace, dev, stream, True)
+    _words(workspace, dev, stream, cu_seqlens is not None)
     return y, st
 
 
@@ -441,8 +438,7 @@ def short_conv_bwd(x, weight, dy, bias=None, s0=None, dst=None, cu_seqlens=None,
     _run(lib.gdn_short_conv_bwd, dev, stream, d, _p(x), _p(weight), _p(bias), _p(s0), _p(cu_seqlens), _p(dy),
          _p(dst), _p(out["dx"]), _p(out["dweight"]), _p(out["dbias"]) if bias is not None else None,
          _p(out["ds0"]), _p(workspace), have)
-    if cu_seqlens is not None:
-        _words(workspace, dev, stream, True)
+    _words(workspace, dev, stream, cu_seqlens is not None)
     return out
 
 

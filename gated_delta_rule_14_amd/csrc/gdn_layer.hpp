@@ -33,8 +33,7 @@ struct Tile {
     int64_t row0;   // first token (row of the activations)
     int n;          // tokens; 0: unused
     int seq;
-    int j;          // tile of its sequence
-    int last;       // 1: the sequence's last tile
+    int j, nt;      // tile j of the nt of its sequence
 };
 
 __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
@@ -45,16 +44,15 @@ __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
         t.n = r.y;
         t.seq = r.z;
         t.j = r.w;
-        t.last = 0;
-        if (r.y > 0) t.last = (int64_t)(r.w + 1) * m.tile >= m.seqs[r.z].y;
+        t.nt = r.y > 0 ? (m.seqs[r.z].y + m.tile - 1) / m.tile : 0;
     } else {
-        const int64_t b = c / m.nt;
-        t.j = (int)(c - b * m.nt);
+        const unsigned nt = (unsigned)m.nt, b = (unsigned)c / nt;   // both below 2^31
+        t.j = (int)((unsigned)c - b * nt);
         t.seq = (int)b;
         const int64_t at = (int64_t)t.j * m.tile;
         t.row0 = b * m.T + at;
         t.n = (int)min((int64_t)m.tile, m.T - at);
-        t.last = t.j == m.nt - 1;
+        t.nt = (int)nt;
     }
     return t;
 }
@@ -78,9 +76,12 @@ struct LinrecLaunch {
     const float *h0 = nullptr, *dht = nullptr;
     void *y = nullptr, *dx = nullptr, *dg = nullptr;
     float *ht = nullptr, *dh0 = nullptr, *dA_log = nullptr, *ddt_bias = nullptr;
-    float* states = nullptr;
-    float* hbuf = nullptr;        // [B*T][D] states of every token (backward)
-    float* part = nullptr;        // [N][2][D] sums of dA_log and ddt_bias (backward)
+    float* states = nullptr;      // [max_tiles][D] the states entering the tiles
+    bool own_states = false;      // backward: states is workspace, to be filled first
+    float* part = nullptr;        // [max_tiles][2][D] sums of dA_log and ddt_bias (backward)
+    // hand-offs between the tiles of a sequence; nullptr where every sequence is one tile
+    uint64_t *pairs = nullptr, *groups = nullptr;   // [max_tiles][D], [max_tiles / 16 + 1][D]
+    int* words = nullptr;         // check of the offsets, failed waits, ticket
     int64_t D = 0, xs = 0, gs = 0, ys = 0;   // channels; token strides of x, g, y / dy
     bool x_bf16 = false, g_bf16 = false;
     hipStream_t stream = nullptr;

@@ -127,21 +127,47 @@ gdn_status check_linrec(const gdn_linrec_desc* d, const gdn_activation* act, gdn
     return GDN_OK;
 }
 
+// Workspace: the words and the tile table, the hand-offs between tiles (where
+// some sequence may have two), and for the backward the states entering the
+// tiles (where the caller kept none) and the tiles' parameter sums.
 struct LinrecLayout {
     TileLayout t;
-    size_t hbuf, part, total;
+    bool hand_offs;
+    size_t pairs, groups, states, part, total;
 };
 LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
     LinrecLayout L;
-    const int64_t N = d->num_seqs > 0 ? d->num_seqs : d->batch, D = d->channels;
+    const int64_t D = d->channels;
     L.t = tile_layout(d->batch, d->seq_len, d->num_seqs, LINREC_TILE);
-    size_t off = L.t.end;
-    L.hbuf = off;
-    if (backward) off += align256((size_t)(d->batch * d->seq_len) * D * 4);
+    L.hand_offs = d->num_seqs > 0 || L.t.nt > 1;
+    size_t off = L.hand_offs || backward ? L.t.end : 0;
+    L.pairs = off;
+    if (L.hand_offs) off += align256((size_t)L.t.tiles * D * 8);
+    L.groups = off;
+    if (L.hand_offs) off += align256((size_t)(L.t.tiles / 16 + 1) * D * 8);
+    L.states = off;
+    if (backward) off += align256((size_t)L.t.tiles * D * 4);
     L.part = off;
-    if (backward) off += align256((size_t)N * 2 * D * 4);
+    if (backward) off += align256((size_t)L.t.tiles * 2 * D * 4);
     L.total = off;
     return L;
+}
+
+// the grids of the tiles, the hand-offs' clearing, the empty sequences and the parameter sums
+gdn_status check_linrec_grid(const gdn_linrec_desc* d, const LinrecLayout& L) {
+    const double D = (double)d->channels, N = (double)(d->num_seqs > 0 ? d->num_seqs : d->batch);
+    gdn_status s = check_grid((double)L.t.tiles * ((D + 63) / 64), 1024);
+    return s != GDN_OK ? s : check_grid(N * ((D + 255) / 256), 256);
+}
+
+void linrec_place(gdn::LinrecLaunch* a, const gdn_linrec_desc* d, const LinrecLayout& L, void* workspace) {
+    char* ws = static_cast<char*>(workspace);
+    a->map = seq_map(L.t, d->batch, d->seq_len, d->num_seqs, LINREC_TILE, workspace);
+    a->words = reinterpret_cast<int*>(ws);
+    if (L.hand_offs) {
+        a->pairs = reinterpret_cast<uint64_t*>(ws + L.pairs);
+        a->groups = reinterpret_cast<uint64_t*>(ws + L.groups);
+    }
 }
 
 gdn::LinrecLaunch linrec_launch(const gdn_linrec_desc* d, const gdn::Act& act, const void* x, const void* g,
@@ -307,10 +333,9 @@ gdn_status gdn_linrec_fwd(const gdn_linrec_desc* d, const gdn_activation* act_in
         return api_fail(GDN_ERR_MISALIGNED, "tensors need their element size, cu_seqlens 8 bytes");
     const LinrecLayout L = linrec_layout(d, false);
     if ((s = check_workspace(workspace, workspace_bytes, L.total)) != GDN_OK) return s;
-    const int64_t N = d->num_seqs > 0 ? d->num_seqs : d->batch;
-    if ((s = check_grid((double)N * (double)((d->channels + 63) / 64), 64)) != GDN_OK) return s;
+    if ((s = check_linrec_grid(d, L)) != GDN_OK) return s;
     gdn::LinrecLaunch a = linrec_launch(d, act, x, g, stream);
-    a.map = seq_map(L.t, d->batch, d->seq_len, d->num_seqs, LINREC_TILE, workspace);
+    linrec_place(&a, d, L, workspace);
     a.h0 = h0;
     a.y = y;
     a.ht = ht;
@@ -338,11 +363,10 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc* d, const gdn_activation* act_in
         return api_fail(GDN_ERR_MISALIGNED, "tensors need their element size, cu_seqlens 8 bytes");
     const LinrecLayout L = linrec_layout(d, true);
     if ((s = check_workspace(workspace, workspace_bytes, L.total)) != GDN_OK) return s;
-    const int64_t N = d->num_seqs > 0 ? d->num_seqs : d->batch;
-    if ((s = check_grid((double)N * (double)((d->channels + 63) / 64), 64)) != GDN_OK) return s;
+    if ((s = check_linrec_grid(d, L)) != GDN_OK) return s;
     gdn::LinrecLaunch a = linrec_launch(d, act, x, g, stream);
     char* ws = static_cast<char*>(workspace);
-    a.map = seq_map(L.t, d->batch, d->seq_len, d->num_seqs, LINREC_TILE, workspace);
+    linrec_place(&a, d, L, workspace);
     a.h0 = h0;
     a.dy = dy;
     a.dht = dht;
@@ -351,8 +375,8 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc* d, const gdn_activation* act_in
     a.dh0 = dh0;
     a.dA_log = dA_log;
     a.ddt_bias = ddt_bias;
-    a.states = const_cast<float*>(states);
-    a.hbuf = reinterpret_cast<float*>(ws + L.hbuf);
+    a.own_states = !states;
+    a.states = states ? const_cast<float*>(states) : reinterpret_cast<float*>(ws + L.states);
     a.part = reinterpret_cast<float*>(ws + L.part);
     if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream)) != GDN_OK) return s;
     hipError_t e = gdn::launch_linrec_bwd(a);

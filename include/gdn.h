@@ -486,6 +486,10 @@ gdn_status gdn_chunk_bwd_act(const gdn_fwd_desc *d, const gdn_activation *act,
  *    decrease and end at seq_len; 1: not) is the first int32 of its
  *    workspace once the stream has reached the call.  Offsets are clamped
  *    into [0, seq_len] as above.
+ *  - The second int32 of a gdn_linrec_fwd / gdn_linrec_bwd workspace is 1 if
+ *    a wait of one workgroup for another gave up (the results are then
+ *    wrong), else 0, once the stream has reached a call that has several
+ *    tiles to a sequence (more than 128 tokens) or packed input.
  *  - Calls that may overlap need workspaces of their own.
  * ====================================================================== */
 
