@@ -99,11 +99,13 @@ struct QkLaunch {
     const void *dqo = nullptr, *dko = nullptr;
     float *dqw = nullptr, *dkw = nullptr, *part = nullptr;
     int64_t tokens, T, Hq, Hk, qs, ks, qhs, khs;
+    int64_t split = 1;            // waves to a token (forward)
     int D, R, norm;
     bool interleaved, bf16;
     float eps, offset;
     hipStream_t stream;
 };
+int64_t qk_bwd_blocks(int64_t tokens);   // rows of part: [2][blocks][D]
 hipError_t launch_qk(const QkLaunch& a);
 hipError_t launch_qk_bwd(const QkLaunch& a);
 

@@ -214,7 +214,7 @@ gdn_status check_qk(const gdn_qk_desc* d) {
         if (h % 8 || ts[i] % 8)
             return api_fail(GDN_ERR_MISALIGNED, "strides must be multiples of 8 elements");
     }
-    return check_grid((double)(d->batch * d->seq_len) * (double)(d->q_heads + d->k_heads), 64);
+    return check_grid(((double)(d->batch * d->seq_len) + 4096) / 4, 256);
 }
 
 gdn::QkLaunch qk_launch(const gdn_qk_desc* d, const void* q, const void* k, const float* qw, const float* kw,
@@ -428,7 +428,7 @@ gdn_status gdn_qk_norm_rope_bwd_workspace(const gdn_qk_desc* d, size_t* bytes) {
     if (!bytes) return api_fail(GDN_ERR_NULL_ARG, "bytes is NULL");
     gdn_status s = check_qk(d);
     if (s != GDN_OK) return s;
-    *bytes = (size_t)(d->batch * d->seq_len) * (d->q_heads + d->k_heads) * d->head_dim * 4;
+    *bytes = align256((size_t)gdn::qk_bwd_blocks(d->batch * d->seq_len) * 2 * d->head_dim * 4);
     return api_ok();
 }
 

@@ -1,127 +1,325 @@
 // Norm of each q and k head and the rotation of its first R elements by
 // position, and its backward pass.
 //
-// One wave per (token, head) row; lane l holds elements l, l + 64, ... so any
-// pair of a rotation is reached through the row in LDS.
+// A wave takes a token: first the token's R/2 angles, one or two to a lane,
+// into LDS, then its heads, 64 / LPR rows at a time with LPR lanes of 8
+// elements to a row (16-byte loads and stores).  The cosines, sines and
+// weights of a lane's 8 elements stay in registers for all heads of the
+// token, so the angle's 64-bit arithmetic is paid once for q_heads + k_heads
+// rows.  Few tokens (decode) split their heads over several waves.
+//
+// The element that a half-split rotation pairs with sits R/16 lanes away and
+// comes by a lane shuffle; interleaved pairs are in the lane itself.
+#include <algorithm>
+
 #include "gdn_layer.hpp"
 
 namespace gdn {
 
 // cos and sin of pos * f: the angle in turns is formed and reduced to
-// [-1/2, 1/2] in 64 bits, so that far positions keep every bit that 32 hold.
-__device__ __forceinline__ void turn(int64_t pos, double f, float* c, float* s) {
+// [-1/2, 1/2] in 64 bits, so that far positions keep every bit that 32 hold
+__device__ __forceinline__ float2 turn(int64_t pos, double f) {
     double t = (double)pos * (f * 0.15915494309189533577);
     t -= rint(t);
-    sincospif((float)(2.0 * t), s, c);
+    float s, c;
+    sincospif((float)(2.0 * t), &s, &c);
+    return make_float2(c, s);
 }
 
-struct Row {
-    bool is_q;
-    int64_t token, head;
+// 8 consecutive elements as loaded
+template <typename T> struct Oct;
+template <> struct Oct<bf16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int e) const { return Vec16<bf16>::get(r, e); }
+    __device__ __forceinline__ static void store(bf16* p, const float* f) {
+        *reinterpret_cast<uint4*>(p) = Vec16<bf16>::pack(f);
+    }
 };
-__device__ __forceinline__ Row row_of(const QkLaunch& p, int64_t i) {
-    const int64_t H = p.Hq + p.Hk, h = i % H;
-    return Row{h < p.Hq, i / H, h < p.Hq ? h : h - p.Hq};
+template <> struct Oct<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float get(int e) const {
+        const float4 v = e < 4 ? a : b;
+        return (e & 3) == 0 ? v.x : (e & 3) == 1 ? v.y : (e & 3) == 2 ? v.z : v.w;
+    }
+    __device__ __forceinline__ static void store(float* p, const float* f) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int off = 1; off < LPR; off <<= 1) v += __shfl_xor(v, off, 64);
+    return v;
 }
 
-template <typename T, bool BWD>
-__global__ __launch_bounds__(64) void qk_kernel(QkLaunch p) {
-    __shared__ float s_row[256];
-    const int lane = threadIdx.x;
-    const Row r = row_of(p, blockIdx.x);
-    const T* x = r.is_q ? static_cast<const T*>(p.q) + r.token * p.qs + r.head * p.qhs
-                        : static_cast<const T*>(p.k) + r.token * p.ks + r.head * p.khs;
-    const int64_t dense = (r.token * (r.is_q ? p.Hq : p.Hk) + r.head) * p.D;
-    T* out = static_cast<T*>(r.is_q ? p.qo : p.ko) + dense;
-    const float* w = r.is_q ? p.qw : p.kw;
-    const int64_t pos = p.positions ? p.positions[r.token] : r.token % p.T;
-    const int half = p.R / 2;
-    float v[4], d[4], ss = 0.f;
-    for (int i = 0; i < 4; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e < p.D ? Elem<T>::load(x + e) : 0.f;
-        ss += v[i] * v[i];
+// What a lane needs of its token: the cosines of its 8 elements (4 pairs when
+// interleaved) and the sines with the sign that its half takes.
+template <bool INTER> struct Spin {
+    float c[8], s[8];
+    int partner;     // lane that holds the other half
+    bool on;         // the lane's elements are rotated (R is a multiple of 16: all or none)
+    // v rotated by the angle (back: by its negative), v as held by the row's lanes
+    template <bool BACK>
+    __device__ __forceinline__ void apply(float* v) const {
+        if (INTER) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = v[2 * j], b = v[2 * j + 1], sj = BACK ? -s[j] : s[j];
+                v[2 * j] = on ? a * c[j] - b * sj : a;
+                v[2 * j + 1] = on ? b * c[j] + a * sj : b;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float o = __shfl(v[e], partner, 64), se = BACK ? -s[e] : s[e];
+                v[e] = on ? v[e] * c[e] + o * se : v[e];
+            }
+        }
     }
-    ss = wave_sum(ss);
-    const float nn = p.norm == GDN_NORM_RMS ? (float)p.D : 1.f;
-    const float rr = p.norm == GDN_NORM_NONE ? 1.f : 1.f / sqrtf(ss / nn + p.eps);
-    const T* dy = nullptr;
-    if (BWD) dy = static_cast<const T*>(r.is_q ? p.dqo : p.dko) + dense;
-    for (int i = 0; i < 4; ++i) {
-        const int e = lane + 64 * i;
-        d[i] = 0.f;
+};
+
+template <bool INTER>
+__device__ __forceinline__ void spin_of(const QkLaunch& p, int64_t token, float2* s_cs, int lane, int sub,
+                                        Spin<INTER>* r) {
+    const int half = p.R / 2, e0 = 8 * sub;
+    __builtin_amdgcn_wave_barrier();   // the wave's LDS accesses stay in order
+    if (half > 0) {
+        const int64_t pos = p.positions ? p.positions[token] : (int64_t)((unsigned)token % (unsigned)p.T);
+        for (int i = lane; i < half; i += 64) s_cs[i] = turn(pos, p.inv_freq[i]);
+    }
+    __builtin_amdgcn_wave_barrier();
+    r->on = e0 < p.R;
+    const bool up = e0 >= half;        // second half of a half-split pair
+    r->partner = INTER || !r->on ? lane : up ? lane - half / 8 : lane + half / 8;
+    const int i0 = !r->on ? 0 : INTER ? e0 / 2 : up ? e0 - half : e0;
+#pragma unroll
+    for (int e = 0; e < (INTER ? 4 : 8); ++e) {
+        const float2 cs = half > 0 ? s_cs[i0 + e] : make_float2(1.f, 0.f);
+        r->c[e] = cs.x;
+        r->s[e] = INTER || up ? cs.y : -cs.y;
+    }
+}
+
+__device__ __forceinline__ void gain_of(const QkLaunch& p, const float* w, int e0, bool live, float* g) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = w && live ? w[e0 + e] + p.offset : 1.f;
+}
+
+__device__ __forceinline__ float norm_of(const QkLaunch& p, float ss, float inv_n) {
+    return p.norm == GDN_NORM_NONE ? 1.f : 1.f / sqrtf(ss * inv_n + p.eps);
+}
+
+// rows [first, last) of one token, a group of 64 / LPR rows after another
+template <typename T, int LPR, bool INTER>
+__device__ __forceinline__ void heads_fwd(const QkLaunch& p, const Spin<INTER>& spin, const T* x, T* out,
+                                          const float* w, int64_t hs, int64_t first, int64_t last, int lane,
+                                          bool live) {
+    constexpr int RPW = 64 / LPR, U = 2;
+    const int sub = lane % LPR, e0 = 8 * sub;
+    const bool in = e0 < p.D;
+    const float inv_n = p.norm == GDN_NORM_RMS ? 1.f / (float)p.D : 1.f;
+    float gain[8];
+    gain_of(p, w, e0, in, gain);
+    for (int64_t h0 = first; h0 < last; h0 += U * RPW) {
+        Oct<T> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t h = h0 + u * RPW + lane / LPR;
+            if (in && h < last) raw[u].load(x + h * hs + e0);
+            else raw[u].zero();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t h = h0 + u * RPW + lane / LPR;
+            float v[8], ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = raw[u].get(e);
+                ss += v[e] * v[e];
+            }
+            const float r = norm_of(p, p.norm == GDN_NORM_NONE ? 0.f : row_sum<LPR>(ss), inv_n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= r * gain[e];
+            spin.template apply<false>(v);
+            if (in && live && h < last) Oct<T>::store(out + h * p.D + e0, v);
+        }
+    }
+}
+
+template <typename T, int LPR, bool INTER>
+__global__ __launch_bounds__(256) void qk_fwd_kernel(QkLaunch p) {
+    __shared__ float2 s_cs[4][128];
+    constexpr int RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const int64_t task = (int64_t)blockIdx.x * 4 + w, all = p.tokens * p.split;
+    const bool live = task < all;
+    const int64_t t = live ? task : all - 1, token = t / p.split, part = t - token * p.split;
+    Spin<INTER> spin;
+    spin_of<INTER>(p, token, s_cs[w], lane, lane % LPR, &spin);
+    // this wave's share of the token's row groups, q's before k's
+    const int64_t gq = (p.Hq + RPW - 1) / RPW, gk = (p.Hk + RPW - 1) / RPW, per = (gq + gk + p.split - 1) / p.split;
+    const int64_t a = part * per, b = min(a + per, gq + gk);
+    if (a < gq)
+        heads_fwd<T, LPR, INTER>(p, spin, static_cast<const T*>(p.q) + token * p.qs,
+                                 static_cast<T*>(p.qo) + token * p.Hq * p.D, p.qw, p.qhs, a * RPW,
+                                 min(b * RPW, p.Hq), lane, live);
+    if (b > gq)
+        heads_fwd<T, LPR, INTER>(p, spin, static_cast<const T*>(p.k) + token * p.ks,
+                                 static_cast<T*>(p.ko) + token * p.Hk * p.D, p.kw, p.khs, (max(a, gq) - gq) * RPW,
+                                 min((b - gq) * RPW, p.Hk), lane, live);
+}
+
+// dn = rotation back of dy; with dw_i = dn_i w_i:
+// dx = r (dw - x r^2/n sum x dw), and the weight's gradient sums dn x r
+template <typename T, int LPR, bool INTER>
+__device__ __forceinline__ void heads_bwd(const QkLaunch& p, const Spin<INTER>& spin, const T* x, const T* dy, T* dx,
+                                          const float* w, int64_t hs, int64_t H, int lane, bool live, float* acc) {
+    constexpr int RPW = 64 / LPR;
+    const int sub = lane % LPR, e0 = 8 * sub;
+    const bool in = e0 < p.D;
+    const float inv_n = p.norm == GDN_NORM_RMS ? 1.f / (float)p.D : 1.f;
+    float gain[8];
+    gain_of(p, w, e0, in, gain);
+    for (int64_t h0 = 0; h0 < H; h0 += RPW) {
+        const int64_t h = h0 + lane / LPR;
+        const bool row = in && live && h < H;
+        Oct<T> rx, rd;
+        if (row) {
+            rx.load(x + h * hs + e0);
+            rd.load(dy + h * p.D + e0);
+        } else {
+            rx.zero();
+            rd.zero();
+        }
+        float v[8], d[8], ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = rx.get(e);
+            d[e] = rd.get(e);
+            ss += v[e] * v[e];
+        }
+        spin.template apply<true>(d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += v[e] * (d[e] * gain[e]);
+        float r = 1.f, k = 0.f;
+        if (p.norm != GDN_NORM_NONE) {
+            r = norm_of(p, row_sum<LPR>(ss), inv_n);
+            k = r * r * inv_n * row_sum<LPR>(dot);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (row) acc[e] += d[e] * (v[e] * r);
+            d[e] = r * (d[e] * gain[e] - v[e] * k);
+        }
+        if (row) Oct<T>::store(dx + h * p.D + e0, d);
+    }
+}
+
+// Waves walk the tokens p.waves apart; a lane's sums for the weights stay in
+// registers until its last token, then meet over the workgroup's rows in LDS.
+template <typename T, int LPR, bool INTER>
+__global__ __launch_bounds__(256) void qk_bwd_kernel(QkLaunch p) {
+    __shared__ float2 s_cs[4][128];
+    __shared__ float s_acc[4 * (64 / LPR)][8 * LPR];
+    constexpr int RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63, w = wave_id(), sub = lane % LPR;
+    float aq[8], ak[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
+    for (int64_t token = (int64_t)blockIdx.x * 4 + w; token < p.tokens; token += (int64_t)gridDim.x * 4) {
+        Spin<INTER> spin;
+        spin_of<INTER>(p, token, s_cs[w], lane, sub, &spin);
+        heads_bwd<T, LPR, INTER>(p, spin, static_cast<const T*>(p.q) + token * p.qs,
+                                 static_cast<const T*>(p.dqo) + token * p.Hq * p.D,
+                                 static_cast<T*>(p.qo) + token * p.Hq * p.D, p.qw, p.qhs, p.Hq, lane, true, aq);
+        heads_bwd<T, LPR, INTER>(p, spin, static_cast<const T*>(p.k) + token * p.ks,
+                                 static_cast<const T*>(p.dko) + token * p.Hk * p.D,
+                                 static_cast<T*>(p.ko) + token * p.Hk * p.D, p.kw, p.khs, p.Hk, lane, true, ak);
+    }
+    if (!p.dqw && !p.dkw) return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_acc[w * RPW + lane / LPR][8 * sub + e] = which ? ak[e] : aq[e];
+        __syncthreads();
+        const int e = threadIdx.x;
         if (e < p.D) {
-            if (BWD) d[i] = Elem<T>::load(dy + e);
-            s_row[e] = BWD ? d[i] : v[i] * rr * (w ? w[e] + p.offset : 1.f);
+            float s = 0.f;
+            for (int i = 0; i < 4 * RPW; ++i) s += s_acc[i][e];
+            p.part[((int64_t)which * gridDim.x + blockIdx.x) * p.D + e] = s;
         }
     }
+}
+
+// the workgroups' sums, 16 strands of workgroups per element, in 64 bits
+__global__ __launch_bounds__(1024) void qk_sum_kernel(QkLaunch p, int64_t blocks) {
+    __shared__ double s[16][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
+    const int64_t which = blockIdx.y;
+    float* out = which ? p.dkw : p.dqw;
+    if (!out) return;
+    double v = 0;
+    if (e < p.D)
+        for (int64_t i = w; i < blocks; i += 16) v += p.part[(which * blocks + i) * p.D + e];
+    s[w][lane] = v;
     __syncthreads();
-    float dot = 0.f;
-    for (int i = 0; i < 4; ++i) {
-        const int e = lane + 64 * i;
-        float y = e < p.D ? s_row[e] : 0.f;
-        if (e < p.R) {
-            const int f = p.interleaved ? e >> 1 : (e < half ? e : e - half);
-            const bool first = p.interleaved ? !(e & 1) : e < half;
-            const float other = s_row[p.interleaved ? e ^ 1 : (first ? e + half : e - half)];
-            float c, s;
-            turn(pos, p.inv_freq[f], &c, &s);
-            if (BWD) s = -s;
-            y = first ? y * c - other * s : y * c + other * s;
-        }
-        if (BWD) {
-            d[i] = y;    // gradient of the normalised, weighted row
-            dot += v[i] * y * (w && e < p.D ? w[e] + p.offset : 1.f);
-        } else if (e < p.D) {
-            Elem<T>::store(out + e, y);
-        }
-    }
-    if (BWD) {
-        dot = p.norm == GDN_NORM_NONE ? 0.f : wave_sum(dot);
-        float* part = r.is_q ? (p.dqw ? p.part : nullptr) : (p.dkw ? p.part : nullptr);
-        for (int i = 0; i < 4; ++i) {
-            const int e = lane + 64 * i;
-            if (e >= p.D) continue;
-            const float dn = d[i] * (w ? w[e] + p.offset : 1.f);
-            Elem<T>::store(out + e, rr * (dn - v[i] * (rr * rr / nn) * dot));
-            if (part) part[(int64_t)blockIdx.x * p.D + e] = d[i] * v[i] * rr;
-        }
-    }
+    if (w != 0 || e >= p.D) return;
+    for (int i = 1; i < 16; ++i) v += s[i][lane];
+    out[e] = (float)v;
 }
 
-__global__ __launch_bounds__(64) void qk_sum_kernel(QkLaunch p) {
-    const int e = blockIdx.x * 64 + threadIdx.x;
-    const bool is_q = blockIdx.y == 0;
-    float* out = is_q ? p.dqw : p.dkw;
-    if (e >= p.D || !out) return;
-    double s = 0;
-    const int64_t H = p.Hq + p.Hk;
-    for (int64_t t = 0; t < p.tokens; ++t)
-        for (int64_t h = is_q ? 0 : p.Hq; h < (is_q ? p.Hq : H); ++h) s += p.part[(t * H + h) * p.D + e];
-    out[e] = (float)s;
-}
-
-hipError_t launch_qk(const QkLaunch& p) {
-    const dim3 grid((unsigned)(p.tokens * (p.Hq + p.Hk)));
-    if (p.bf16)
-        hipLaunchKernelGGL((qk_kernel<bf16, false>), grid, dim3(64), 0, p.stream, p);
-    else
-        hipLaunchKernelGGL((qk_kernel<float, false>), grid, dim3(64), 0, p.stream, p);
+template <typename T, int LPR, bool INTER>
+static hipError_t go2(const QkLaunch& p, bool bwd) {
+    if (bwd) {
+        hipLaunchKernelGGL((qk_bwd_kernel<T, LPR, INTER>), dim3((unsigned)qk_bwd_blocks(p.tokens)), dim3(256), 0,
+                           p.stream, p);
+    } else {
+        // Waves for at least half of the chip's slots: decode's few tokens share their row
+        // groups out, one to a wave at most.
+        QkLaunch a = p;
+        const int64_t rpw = 64 / LPR, groups = (p.Hq + rpw - 1) / rpw + (p.Hk + rpw - 1) / rpw;
+        a.split = std::min(groups, std::max((int64_t)1, 4096 / p.tokens));
+        hipLaunchKernelGGL((qk_fwd_kernel<T, LPR, INTER>), dim3((unsigned)((p.tokens * a.split + 3) / 4)), dim3(256),
+                           0, p.stream, a);
+    }
     return hipGetLastError();
 }
+template <typename T, bool INTER>
+static hipError_t go1(const QkLaunch& p, bool bwd) {
+    if (p.D <= 32) return go2<T, 4, INTER>(p, bwd);
+    if (p.D <= 64) return go2<T, 8, INTER>(p, bwd);
+    if (p.D <= 128) return go2<T, 16, INTER>(p, bwd);
+    return go2<T, 32, INTER>(p, bwd);
+}
+static hipError_t go(const QkLaunch& p, bool bwd) {
+    if (p.bf16) return p.interleaved ? go1<bf16, true>(p, bwd) : go1<bf16, false>(p, bwd);
+    return p.interleaved ? go1<float, true>(p, bwd) : go1<float, false>(p, bwd);
+}
+
+// Workgroups of the backward: two waves of tokens for every slot of the chip
+// at most, so that the sums over tokens stay in registers.
+int64_t qk_bwd_blocks(int64_t tokens) { return std::min((tokens + 3) / 4, (int64_t)2048); }
+
+hipError_t launch_qk(const QkLaunch& p) { return go(p, false); }
 
 hipError_t launch_qk_bwd(const QkLaunch& p) {
-    const dim3 grid((unsigned)(p.tokens * (p.Hq + p.Hk)));
     if (p.tokens > 0) {
-        if (p.bf16)
-            hipLaunchKernelGGL((qk_kernel<bf16, true>), grid, dim3(64), 0, p.stream, p);
-        else
-            hipLaunchKernelGGL((qk_kernel<float, true>), grid, dim3(64), 0, p.stream, p);
-        hipError_t e = hipGetLastError();
+        hipError_t e = go(p, true);
         if (e != hipSuccess) return e;
     }
     if (!p.dqw && !p.dkw) return hipSuccess;
-    hipLaunchKernelGGL(qk_sum_kernel, dim3((unsigned)((p.D + 63) / 64), 2), dim3(64), 0, p.stream, p);
+    hipLaunchKernelGGL(qk_sum_kernel, dim3((unsigned)((p.D + 63) / 64), 2), dim3(1024), 0, p.stream, p,
+                       qk_bwd_blocks(p.tokens));
     return hipGetLastError();
 }
 
