@@ -305,6 +305,13 @@ gdn::ConvLaunch conv_launch(const gdn_conv_desc* d, const void* x, const float* 
     return a;
 }
 
+// the grids of the tiles, the empty sequences and the parameter sums
+gdn_status check_conv_grid(const gdn::ConvLaunch& a) {
+    gdn_status s = check_grid((double)a.map.max_tiles * (double)((a.D + 63) / 64), 64);
+    if (s == GDN_OK) s = check_grid((double)a.map.N * (double)(((a.W - 1) * a.D + 255) / 256), 256);
+    return s != GDN_OK ? s : check_grid((double)(a.W + 1) * (double)((a.D + 63) / 64), 1024);
+}
+
 }  // namespace
 
 extern "C" {
@@ -481,7 +488,7 @@ gdn_status gdn_short_conv_fwd(const gdn_conv_desc* d, const void* x, const float
     if ((s = check_workspace(workspace, workspace_bytes, L.total)) != GDN_OK) return s;
     gdn::ConvLaunch a = conv_launch(d, x, weight, bias, s0, stream);
     a.map = seq_map(L.t, d->batch, d->seq_len, d->num_seqs, CONV_TILE, workspace);
-    if ((s = check_grid((double)(a.map.max_tiles + a.map.N) * (double)((a.D + 63) / 64), 64)) != GDN_OK) return s;
+    if ((s = check_conv_grid(a)) != GDN_OK) return s;
     a.y = y;
     a.st = st;
     if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream)) != GDN_OK) return s;
@@ -509,7 +516,7 @@ gdn_status gdn_short_conv_bwd(const gdn_conv_desc* d, const void* x, const float
     if ((s = check_workspace(workspace, workspace_bytes, L.total)) != GDN_OK) return s;
     gdn::ConvLaunch a = conv_launch(d, x, weight, bias, s0, stream);
     a.map = seq_map(L.t, d->batch, d->seq_len, d->num_seqs, CONV_TILE, workspace);
-    if ((s = check_grid((double)(a.map.max_tiles + a.map.N) * (double)((a.D + 63) / 64), 64)) != GDN_OK) return s;
+    if ((s = check_conv_grid(a)) != GDN_OK) return s;
     a.dy = dy;
     a.dst = dst;
     a.dx = dx;
