@@ -36,15 +36,17 @@ struct Tile {
     int j, nt;      // tile j of the nt of its sequence
 };
 
+// c is the same for the whole wave, and so is what comes back: in scalar
+// registers, for the row addresses
 __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
     Tile t;
     if (m.table) {
         const int4 r = m.table[c];
-        t.row0 = r.x;
-        t.n = r.y;
-        t.seq = r.z;
-        t.j = r.w;
-        t.nt = r.y > 0 ? (m.seqs[r.z].y + m.tile - 1) / m.tile : 0;
+        t.row0 = __builtin_amdgcn_readfirstlane(r.x);
+        t.n = __builtin_amdgcn_readfirstlane(r.y);
+        t.seq = __builtin_amdgcn_readfirstlane(r.z);
+        t.j = __builtin_amdgcn_readfirstlane(r.w);
+        t.nt = t.n > 0 ? (__builtin_amdgcn_readfirstlane(m.seqs[t.seq].y) + m.tile - 1) / m.tile : 0;
     } else {
         const unsigned nt = (unsigned)m.nt, b = (unsigned)c / nt;   // both below 2^31
         t.j = (int)((unsigned)c - b * nt);

@@ -25,9 +25,9 @@ gdn_status check_rows(int64_t B, int64_t T, int64_t D, int64_t N, bool packed) {
     if (packed && (B != 1 || N <= 0))
         return api_fail(GDN_ERR_BAD_SHAPE, "packed sequences need batch == 1 and num_seqs > 0");
     if (!packed && N != 0) return api_fail(GDN_ERR_BAD_SHAPE, "num_seqs must be 0 without cu_seqlens");
-    const int64_t lim = (int64_t)1 << 31;
-    if (B >= lim || T >= lim || D >= lim || N >= lim || B * T >= lim)
-        return api_fail(GDN_ERR_BAD_SHAPE, "B*T, channels and num_seqs must be below 2^31");
+    const int64_t lim = (int64_t)1 << 31;   // channels: byte offsets in a row are 32-bit
+    if (B >= lim || T >= lim || D >= (lim >> 3) || N >= lim || B * T >= lim)
+        return api_fail(GDN_ERR_BAD_SHAPE, "B*T and num_seqs must be below 2^31, channels below 2^28");
     return GDN_OK;
 }
 

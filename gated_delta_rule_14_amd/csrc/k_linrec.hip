@@ -33,43 +33,43 @@ constexpr unsigned ABSENT = 0xffffffffu;     // never the bits of a published A
 constexpr int POLLS = 1 << 20;               // about a second; a hand-off takes microseconds
 
 // ---- gates
-// All of the gate's functions come from the hardware's exp2, reciprocal and
-// square root (1 unit in the last place each) and series that hold the
-// leading bits where the direct formula cancels.
-__device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
-__device__ __forceinline__ float sqrt_hw(float x) { return __builtin_amdgcn_sqrtf(x); }
+// Everything in the log2 domain: the hardware's exp2, reciprocal and reciprocal
+// square root (1 unit in the last place each) and two polynomials where a
+// direct formula would cancel. Their coefficients are least-squares fits to
+// the function over the stated range, reweighted towards the least largest
+// relative error; evaluated in 32 bits both are within 2.5 half units.
 
-// log1p(e), 0 <= e <= 1: 2 artanh(s), s = e / (2 + e) <= 1/3; the first term
-// left out is s^16/17 < 2e-9 of the sum
+// log1p(e), 0 <= e <= 1: no reciprocal, as a quotient form would need
 __device__ __forceinline__ float log1p_unit(float e) {
-    const float s = e * rcp_hw(2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = p * q + 1.f / 13.f;
-    p = p * q + 1.f / 11.f;
-    p = p * q + 1.f / 9.f;
-    p = p * q + 1.f / 7.f;
-    p = p * q + 1.f / 5.f;
-    p = p * q + 1.f / 3.f;
-    return 2.f * s + 2.f * s * (q * p);
+    float p = -0.0032440086360021803f;
+    p = p * e + 0.019851388409733772f;
+    p = p * e - 0.05695939436554909f;
+    p = p * e + 0.10603640973567963f;
+    p = p * e - 0.1530558466911316f;
+    p = p * e + 0.19675935804843903f;
+    p = p * e - 0.24954132735729218f;
+    p = p * e + 0.3332996368408203f;
+    p = p * e - 0.4999990165233612f;
+    p = p * e + 1.f;
+    return p * e;
 }
 
-// 1 - exp(t) for t <= 0, et = exp(t): the series of -expm1 above -0.35, where
-// 1 - et would cancel (first term left out: t^7/8! < 2e-8 of the sum)
-__device__ __forceinline__ float one_minus_exp(float t, float et) {
-    float p = 1.f / 5040.f;
-    p = p * t + 1.f / 720.f;
-    p = p * t + 1.f / 120.f;
-    p = p * t + 1.f / 24.f;
-    p = p * t + 1.f / 6.f;
-    p = p * t + 0.5f;
-    p = p * t + 1.f;
-    return t > -0.35f ? -t * p : 1.f - et;
+// 1 - a^2 from l = log2 a: a polynomial times -l for a^2 > 0.7, where 1 - a^2 would cancel
+__device__ __forceinline__ float one_minus_sq(float l, float a) {
+    float p = 0.03694247081875801f;
+    p = p * l + 0.15266050398349762f;
+    p = p * l + 0.4439232647418976f;
+    p = p * l + 0.9609025716781616f;
+    p = p * l + 1.3862943649291992f;
+    float near = -l * p, far = 1.f - a * a;
+    asm("" : "+v"(near), "+v"(far));       // both, and a select: a branch per element costs more
+    return l > -0.25f ? near : far;
 }
 
 constexpr float LN2 = 0.6931471805599453f;
 
 struct Gate {
-    float la;      // log a
+    float l2;      // log2 a
     float a;
     float m;       // factor of x
     float sg;      // sigmoid(g + bias): d log a / d g = rate sg
@@ -78,52 +78,68 @@ struct Gate {
 template <bool ACT, bool NORM, bool BWD>
 __device__ __forceinline__ Gate gate_of(float g, float rate2, float bias) {
     Gate r;
-    float l2;
     r.sg = 0.f;
     if (ACT) {
         const float z = g + bias, e = exp2_hw(-LOG2E * fabsf(z));
-        l2 = rate2 * (fmaxf(z, 0.f) + log1p_unit(e));
-        if (BWD) r.sg = (z >= 0.f ? 1.f : e) * rcp_hw(1.f + e);
-        r.la = LN2 * l2;
+        r.l2 = rate2 * (fmaxf(z, 0.f) + log1p_unit(e));
+        if (BWD) r.sg = (z >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
     } else {
-        l2 = g * LOG2E;
-        r.la = g;
+        r.l2 = g * LOG2E;
     }
-    r.a = exp2_hw(l2);
-    r.m = NORM ? sqrt_hw(fmaxf(one_minus_exp(2.f * r.la, r.a * r.a), 0.f)) : 1.f;
+    r.a = exp2_hw(r.l2);
+    r.m = NORM ? __builtin_amdgcn_sqrtf(one_minus_sq(r.l2, r.a)) : 1.f;
     return r;
 }
 
-// ---- V consecutive elements as loaded, and their floats
+// ---- V consecutive elements as loaded, and their floats.  A row is the same
+// for the whole wave (a scalar base), the channel a 32-bit byte offset of it.
+// The row's address, held in scalar registers: left to itself the compiler adds
+// the channel to the tile's base first, and a row then costs a 64-bit vector
+// addition and two vector registers while its load is in flight.
+template <typename T> __device__ __forceinline__ T* in_scalar(T* row) {
+    asm("" : "+s"(row));
+    return row;
+}
+#define GDN_GLOBAL __attribute__((address_space(1)))
+template <typename U> __device__ __forceinline__ U peek_row(const void* row, unsigned off) {
+    return *(const GDN_GLOBAL U*)((const GDN_GLOBAL char*)row + off);
+}
+template <typename U> __device__ __forceinline__ void poke_row(void* row, unsigned off, U v) {
+    *(GDN_GLOBAL U*)((GDN_GLOBAL char*)row + off) = v;
+}
 template <typename T, int V> struct Raw;
 template <> struct Raw<bf16, 1> {
     uint32_t r;
-    __device__ __forceinline__ void load(const bf16* p) { r = p->bits; }
+    __device__ __forceinline__ void load(const bf16* row, unsigned off) { r = peek_row<uint16_t>(row, off); }
     __device__ __forceinline__ float get(int) const { return __uint_as_float(r << 16); }
-    __device__ __forceinline__ static void store(bf16* p, const float* f) { p->bits = f32_to_bf16(f[0]); }
+    __device__ __forceinline__ static void store(bf16* row, unsigned off, const float* f) {
+        poke_row<uint16_t>(row, off, f32_to_bf16(f[0]));
+    }
 };
 template <> struct Raw<bf16, 2> {
     uint32_t r;
-    __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void load(const bf16* row, unsigned off) { r = peek_row<uint32_t>(row, off); }
     __device__ __forceinline__ float get(int e) const {
         return __uint_as_float(e ? r & 0xffff0000u : r << 16);
     }
-    __device__ __forceinline__ static void store(bf16* p, const float* f) {
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
+    __device__ __forceinline__ static void store(bf16* row, unsigned off, const float* f) {
+        poke_row<uint32_t>(row, off, pack_bf16x2(f[0], f[1]));
     }
 };
 template <> struct Raw<float, 1> {
     float r;
-    __device__ __forceinline__ void load(const float* p) { r = *p; }
+    __device__ __forceinline__ void load(const float* row, unsigned off) { r = peek_row<float>(row, off); }
     __device__ __forceinline__ float get(int) const { return r; }
-    __device__ __forceinline__ static void store(float* p, const float* f) { *p = f[0]; }
+    __device__ __forceinline__ static void store(float* row, unsigned off, const float* f) {
+        poke_row<float>(row, off, f[0]);
+    }
 };
 template <> struct Raw<float, 2> {
     float2 r;
-    __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void load(const float* row, unsigned off) { r = __builtin_bit_cast(float2, peek_row<f32x2v>(row, off)); }
     __device__ __forceinline__ float get(int e) const { return e ? r.y : r.x; }
-    __device__ __forceinline__ static void store(float* p, const float* f) {
-        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+    __device__ __forceinline__ static void store(float* row, unsigned off, const float* f) {
+        poke_row<f32x2v>(row, off, f32x2v{f[0], f[1]});
     }
 };
 
@@ -194,19 +210,29 @@ __device__ __forceinline__ float enter(const LinrecLaunch& p, int64_t tile, int 
     return ng == 0 ? gH : gA * v + gH;
 }
 
-// Every pair that some tile reads is marked absent, the ticket and the words cleared.
-__global__ __launch_bounds__(256) void linrec_clear_kernel(LinrecLaunch p) {
-    const int64_t nb = (p.D + 255) / 256, tile = blockIdx.x / nb, c = (blockIdx.x - tile * nb) * 256 + threadIdx.x;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+// Every pair that some tile reads is marked absent, the ticket and the words
+// are cleared; and sequences without a token hand their state through
+// (forward: ht = h0, backward: dh0 = dht), by the workgroups past the tiles'.
+__global__ __launch_bounds__(256) void linrec_clear_kernel(LinrecLaunch p, const float* from, float* to) {
+    const unsigned nb = (unsigned)((p.D + 511) / 512), i = blockIdx.x / nb;
+    const int64_t c0 = (int64_t)(blockIdx.x - i * nb) * 512 + threadIdx.x;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.pairs) {
         if (!p.map.table) p.words[0] = 0;
         p.words[1] = 0;
         p.words[2] = 0;
     }
-    if (c >= p.D) return;
-    const Tile t = tile_of(p.map, tile);
-    if (t.n > 0 && t.nt > 1) {
-        p.pairs[tile * p.D + c] = ABSENT;
-        if (t.nt > GROUP) p.groups[(tile / GROUP) * p.D + c] = ABSENT;
+    const int64_t tiles = p.pairs ? p.map.max_tiles : 0;
+    if (i >= tiles) {
+        const int64_t n = i - tiles;
+        if ((p.map.seqs ? p.map.seqs[n].y : p.map.T) > 0) return;
+        for (int64_t c = c0; c < min(c0 + 512, p.D); c += 256) to[n * p.D + c] = from ? from[n * p.D + c] : 0.f;
+        return;
+    }
+    const Tile t = tile_of(p.map, i);
+    if (t.n <= 0 || t.nt <= 1) return;
+    for (int64_t c = c0; c < min(c0 + 512, p.D); c += 256) {
+        p.pairs[i * p.D + c] = ABSENT;
+        if (t.nt > GROUP) p.groups[(i / GROUP) * p.D + c] = ABSENT;
     }
 }
 
@@ -218,36 +244,50 @@ __device__ __forceinline__ unsigned ticket_of(const LinrecLaunch& p, unsigned* s
     return __builtin_amdgcn_readfirstlane(*s);
 }
 
-template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
-__global__ __launch_bounds__(64 * NW) void linrec_fwd_kernel(LinrecLaunch p) {
-    constexpr int CB = 64 * V;
-    static_assert(CB <= 64 * NW, "one thread per channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_in[CB];
-    __shared__ unsigned s_ticket;
-    const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB);
-    const unsigned tile = k / nb;
-    const int64_t c0 = (int64_t)(k - tile * nb) * CB;
-    const Tile t = tile_of(p.map, tile);
-    if (t.n <= 0) return;
-    const int w = wave_id(), lane = threadIdx.x & 63;
-    const int64_t cl = c0 + lane * V, c = min(cl, p.D - V);   // idle lanes repeat the last channels
-    const int first = w * S, nv = min(S, t.n - first);        // this wave's tokens (may be none)
+// A wave's place in its tile.
+struct Spot {
+    int w, lane, first, nv;   // wave, lane; first token in the tile; its tokens (0 and less: none)
+    int64_t c0, c;            // first channel of the block; of the lane (idle lanes repeat the last)
+    bool in;                  // the lane has channels
+};
+template <int V, int S>
+__device__ __forceinline__ Spot spot_of(const LinrecLaunch& p, const Tile& t, int64_t c0) {
+    Spot s;
+    s.w = wave_id();
+    s.lane = threadIdx.x & 63;
+    s.first = s.w * S;
+    s.nv = min(S, t.n - s.first);
+    s.c0 = c0;
+    s.in = c0 + s.lane * V < p.D;
+    s.c = min(c0 + s.lane * V, p.D - V);
+    return s;
+}
+// rows of the wave's tokens; of a tile that is not FULL the last one again past its end
+template <bool FULL, typename T>
+__device__ __forceinline__ const T* row_at(const T* tile, int64_t stride, const Spot& s, const Tile& t, int i) {
+    return in_scalar(tile + (int64_t)(FULL ? s.first + i : min(s.first + i, t.n - 1)) * stride);
+}
 
-    Raw<X, V> rx[S];
-    Raw<G, V> rg[S];
+template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+__device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
+                                         float (*s_A)[64 * V], float (*s_H)[64 * V], float* s_in) {
+    constexpr int CB = 64 * V;
+    const Spot s = spot_of<V, S>(p, t, c0);
     const X* x = static_cast<const X*>(p.x) + t.row0 * p.xs;
     const G* g = static_cast<const G*>(p.g) + t.row0 * p.gs;
+    const unsigned ox = (unsigned)s.c * sizeof(X), og = (unsigned)s.c * sizeof(G);
+    Raw<X, V> rx[S];
+    Raw<G, V> rg[S];
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-        const int64_t r = min(first + i, t.n - 1);            // rows past the tile: loaded, not used
-        rx[i].load(x + r * p.xs + c);
-        rg[i].load(g + r * p.gs + c);
+        rg[i].load(row_at<FULL>(g, p.gs, s, t, i), og);
+        rx[i].load(row_at<FULL>(x, p.xs, s, t, i), ox);
     }
     float rate2[V], bias[V], A[V], H[V], a[S][V], u[S][V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        rate2[e] = ACT ? -LOG2E * expf(p.act.A_log[c + e]) : 0.f;
-        bias[e] = ACT ? p.act.dt_bias[c + e] : 0.f;
+        rate2[e] = ACT ? -LOG2E * expf(p.act.A_log[s.c + e]) : 0.f;
+        bias[e] = ACT ? p.act.dt_bias[s.c + e] : 0.f;
         A[e] = 1.f;
         H[e] = 0.f;
     }
@@ -256,23 +296,23 @@ __global__ __launch_bounds__(64 * NW) void linrec_fwd_kernel(LinrecLaunch p) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const Gate q = gate_of<ACT, NORM, false>(rg[i].get(e), rate2[e], bias[e]);
-            a[i][e] = i < nv ? q.a : 1.f;
-            u[i][e] = i < nv ? q.m * rx[i].get(e) : 0.f;
+            a[i][e] = FULL || i < s.nv ? q.a : 1.f;
+            u[i][e] = FULL || i < s.nv ? q.m * rx[i].get(e) : 0.f;
             H[e] = a[i][e] * H[e] + u[i][e];
             A[e] *= a[i][e];
         }
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        s_A[w][lane * V + e] = A[e];
-        s_H[w][lane * V + e] = H[e];
+        s_A[s.w][s.lane * V + e] = A[e];
+        s_H[s.w][s.lane * V + e] = H[e];
     }
     __syncthreads();
     const int tid = threadIdx.x;
     if (tid < CB && c0 + tid < p.D) {
         const int64_t cc = c0 + tid;
         float tA = 1.f, tH = 0.f;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < NW; ++i) {
             tH = s_A[i][tid] * tH + s_H[i][tid];
             tA *= s_A[i][tid];
@@ -285,96 +325,99 @@ __global__ __launch_bounds__(64 * NW) void linrec_fwd_kernel(LinrecLaunch p) {
     }
     if (!p.y) return;
     __syncthreads();
-    if (cl >= p.D) return;
-    X* y = static_cast<X*>(p.y) + (t.row0 + first) * p.ys + c;
     float h[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        h[e] = s_in[lane * V + e];
-        for (int i = 0; i < w; ++i) h[e] = s_A[i][lane * V + e] * h[e] + s_H[i][lane * V + e];
+        h[e] = s_in[s.lane * V + e];
+        for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
     }
+    if (!s.in) return;
+    X* y = static_cast<X*>(p.y) + (t.row0 + s.first) * p.ys;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
 #pragma unroll
         for (int e = 0; e < V; ++e) h[e] = a[i][e] * h[e] + u[i][e];
-        if (i < nv) Raw<X, V>::store(y + i * p.ys, h);
+        if (FULL || i < s.nv) Raw<X, V>::store(in_scalar(y + i * p.ys), ox, h);
     }
+}
+
+template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+__global__ __launch_bounds__(64 * NW) void linrec_fwd_kernel(LinrecLaunch p) {
+    constexpr int CB = 64 * V;
+    static_assert(CB <= 64 * NW, "one thread per channel of the block");
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_in[CB];
+    __shared__ unsigned s_ticket;
+    const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB), tile = k / nb;
+    const int64_t c0 = (int64_t)(k - tile * nb) * CB;
+    const Tile t = tile_of(p.map, tile);
+    if (t.n <= 0) return;
+    if (t.n == S * NW) fwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_in);
+    else fwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_in);
 }
 
 // The same tiles taken from the last token: e = a (dy + e') is what a token
 // hands to the one before it, again a composition of affine maps, with the
 // same A.  The states before each token come from the state entering the
 // tile, kept by the forward.
-template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
-__global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
+template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+__device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
+                                         float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_E)[64 * V],
+                                         float* s_in, float* s_e, f32x2v (*s_gate)[64 * NW]) {
     constexpr int CB = 64 * V;
-    static_assert(CB <= 64 * NW, "one thread per channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB], s_in[CB], s_e[CB];
-    __shared__ unsigned s_ticket;
-    const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB);
-    const unsigned tile = (unsigned)p.map.max_tiles - 1 - k / nb;
-    const int64_t c0 = (int64_t)(k % nb) * CB;
-    const Tile t = tile_of(p.map, tile);
-    const int w = wave_id(), lane = threadIdx.x & 63, tid = threadIdx.x;
-    if (t.n <= 0) {
-        if (ACT && tid < CB && c0 + tid < p.D) {
-            p.part[(int64_t)(2 * tile) * p.D + c0 + tid] = 0.f;
-            p.part[(int64_t)(2 * tile + 1) * p.D + c0 + tid] = 0.f;
-        }
-        return;
-    }
-    const int64_t cl = c0 + lane * V, c = min(cl, p.D - V);
-    const int first = w * S, nv = min(S, t.n - first);
-
-    Raw<X, V> rx[S], rd[S];
-    Raw<G, V> rg[S];
+    const Spot s = spot_of<V, S>(p, t, c0);
+    const int tid = threadIdx.x;
     const X* x = static_cast<const X*>(p.x) + t.row0 * p.xs;
     const G* g = static_cast<const G*>(p.g) + t.row0 * p.gs;
     const X* dy = static_cast<const X*>(p.dy) + t.row0 * p.ys;
+    const unsigned ox = (unsigned)s.c * sizeof(X), og = (unsigned)s.c * sizeof(G);
+    Raw<X, V> rx[S], rd[S];
+    float a[S][V], m[S][V];
+    float rate2[V], bias[V], A[V], H[V], E[V];
+    {
+        Raw<G, V> rg[S];
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const int64_t r = min(first + i, t.n - 1);
-        rg[i].load(g + r * p.gs + c);
-        rx[i].load(x + r * p.xs + c);
-        rd[i].load(dy + r * p.ys + c);
-    }
-    float rate2[V], bias[V], A[V], H[V], E[V], a[S][V], la[S][V], m[S][V], sg[S][V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        rate2[e] = ACT ? -LOG2E * expf(p.act.A_log[c + e]) : 0.f;
-        bias[e] = ACT ? p.act.dt_bias[c + e] : 0.f;
-        A[e] = 1.f;
-        H[e] = 0.f;
-        E[e] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < S; ++i) {
+            rg[i].load(row_at<FULL>(g, p.gs, s, t, i), og);
+            rx[i].load(row_at<FULL>(x, p.xs, s, t, i), ox);
+            rd[i].load(row_at<FULL>(dy, p.ys, s, t, i), ox);
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const Gate q = gate_of<ACT, NORM, true>(rg[i].get(e), rate2[e], bias[e]);
-            a[i][e] = i < nv ? q.a : 1.f;
-            m[i][e] = q.m;
-            la[i][e] = q.la;
-            sg[i][e] = q.sg;
-            H[e] = a[i][e] * H[e] + (i < nv ? q.m * rx[i].get(e) : 0.f);
-            A[e] *= a[i][e];
+            rate2[e] = ACT ? -LOG2E * expf(p.act.A_log[s.c + e]) : 0.f;
+            bias[e] = ACT ? p.act.dt_bias[s.c + e] : 0.f;
+            A[e] = 1.f;
+            H[e] = 0.f;
+            E[e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const Gate q = gate_of<ACT, NORM, true>(rg[i].get(e), rate2[e], bias[e]);
+                a[i][e] = FULL || i < s.nv ? q.a : 1.f;
+                m[i][e] = q.m;
+                if (ACT) s_gate[i * V + e][tid] = f32x2v{q.l2, q.sg};
+                H[e] = a[i][e] * H[e] + (FULL || i < s.nv ? q.m * rx[i].get(e) : 0.f);
+                A[e] *= a[i][e];
+            }
+            __builtin_amdgcn_sched_barrier(0);   // a token at a time: registers, not overlap, are short
         }
     }
 #pragma unroll
     for (int i = S - 1; i >= 0; --i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) E[e] = a[i][e] * ((i < nv ? rd[i].get(e) : 0.f) + E[e]);
+        for (int e = 0; e < V; ++e) E[e] = a[i][e] * ((FULL || i < s.nv ? rd[i].get(e) : 0.f) + E[e]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        s_A[w][lane * V + e] = A[e];
-        s_H[w][lane * V + e] = H[e];
-        s_E[w][lane * V + e] = E[e];
+        s_A[s.w][s.lane * V + e] = A[e];
+        s_H[s.w][s.lane * V + e] = H[e];
+        s_E[s.w][s.lane * V + e] = E[e];
     }
     __syncthreads();
     if (tid < CB && c0 + tid < p.D) {
         const int64_t cc = c0 + tid;
         float tA = 1.f, tE = 0.f;
-#pragma unroll
+#pragma unroll 2
         for (int i = NW - 1; i >= 0; --i) {
             tE = s_A[i][tid] * tE + s_E[i][tid];
             tA *= s_A[i][tid];
@@ -387,14 +430,13 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
         if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + cc] = tA * in + tE;
     }
     __syncthreads();
-    float h[V], d[V], sA[V], sb[V];
-    float before[S][V];
+    float h[V], d[V], sA[V], sb[V], before[S][V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        h[e] = s_in[lane * V + e];
-        d[e] = s_e[lane * V + e];
-        for (int i = 0; i < w; ++i) h[e] = s_A[i][lane * V + e] * h[e] + s_H[i][lane * V + e];
-        for (int i = NW - 1; i > w; --i) d[e] = s_A[i][lane * V + e] * d[e] + s_E[i][lane * V + e];
+        h[e] = s_in[s.lane * V + e];
+        d[e] = s_e[s.lane * V + e];
+        for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
+        for (int i = NW - 1; i > s.w; --i) d[e] = s_A[i][s.lane * V + e] * d[e] + s_E[i][s.lane * V + e];
         sA[e] = 0.f;
         sb[e] = 0.f;
     }
@@ -405,36 +447,40 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
             before[i][e] = h[e];
             h[e] = a[i][e] * h[e] + m[i][e] * rx[i].get(e);
         }
-    X* dx = static_cast<X*>(p.dx) + (t.row0 + first) * p.D + c;
-    G* dg = static_cast<G*>(p.dg) + (t.row0 + first) * p.D + c;
+    X* dx = static_cast<X*>(p.dx) + (t.row0 + s.first) * p.D;
+    G* dg = static_cast<G*>(p.dg) + (t.row0 + s.first) * p.D;
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
-        if (i >= nv) continue;
-        float ox[V], og[V];
+        if (!FULL && i >= s.nv) continue;
+        float vx[V], vg[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float dh = rd[i].get(e) + d[e];
             d[e] = a[i][e] * dh;
             float dla = d[e] * before[i][e];
-            if (NORM) dla -= m[i][e] > 0.f ? d[e] * rx[i].get(e) * (a[i][e] * rcp_hw(m[i][e])) : 0.f;
-            ox[e] = m[i][e] * dh;
-            og[e] = ACT ? dla * (LN2 * rate2[e]) * sg[i][e] : dla;
+            if (NORM)
+                dla -= m[i][e] > 0.f ? d[e] * rx[i].get(e) * (a[i][e] * __builtin_amdgcn_rcpf(m[i][e])) : 0.f;
+            vx[e] = m[i][e] * dh;
+            vg[e] = dla;
             if (ACT) {
-                sA[e] += dla * la[i][e];
-                sb[e] += og[e];
+                const f32x2v q = s_gate[i * V + e][tid];
+                vg[e] = dla * (LN2 * rate2[e]) * q.y;
+                sA[e] += dla * q.x;
+                sb[e] += vg[e];
             }
         }
-        if (cl < p.D) {
-            Raw<X, V>::store(dx + i * p.D, ox);
-            Raw<G, V>::store(dg + i * p.D, og);
+        if (s.in) {
+            Raw<X, V>::store(in_scalar(dx + i * p.D), ox, vx);
+            Raw<G, V>::store(in_scalar(dg + i * p.D), og, vg);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
     if (!ACT) return;
     __syncthreads();                                          // the waves have read the pairs
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        s_A[w][lane * V + e] = sA[e];
-        s_H[w][lane * V + e] = sb[e];
+        s_A[s.w][s.lane * V + e] = sA[e];
+        s_H[s.w][s.lane * V + e] = sb[e];
     }
     __syncthreads();
     if (tid < CB && c0 + tid < p.D) {
@@ -444,9 +490,34 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
             tA += s_A[i][tid];
             tb += s_H[i][tid];
         }
-        p.part[(int64_t)(2 * tile) * p.D + c0 + tid] = tA;
-        p.part[(int64_t)(2 * tile + 1) * p.D + c0 + tid] = tb;
+        p.part[2 * tile * p.D + c0 + tid] = LN2 * tA;
+        p.part[(2 * tile + 1) * p.D + c0 + tid] = tb;
     }
+}
+
+template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+__global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
+    constexpr int CB = 64 * V;
+    static_assert(CB <= 64 * NW, "one thread per channel of the block");
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB], s_in[CB], s_e[CB];
+    // log2 a and sigmoid of every token, each thread's own: they are wanted again only at
+    // the end, and next to a, m, x and dy there are no registers for them
+    __shared__ f32x2v s_gate[ACT ? S * V : 1][64 * NW];
+    __shared__ unsigned s_ticket;
+    const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB);
+    const unsigned tile = (unsigned)p.map.max_tiles - 1 - k / nb;
+    const int64_t c0 = (int64_t)(k % nb) * CB;
+    const Tile t = tile_of(p.map, tile);
+    const int tid = threadIdx.x;
+    if (t.n <= 0) {
+        if (ACT && tid < CB && c0 + tid < p.D) {
+            p.part[(int64_t)(2 * tile) * p.D + c0 + tid] = 0.f;
+            p.part[(int64_t)(2 * tile + 1) * p.D + c0 + tid] = 0.f;
+        }
+        return;
+    }
+    if (t.n == S * NW) bwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_in, s_e, s_gate);
+    else bwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_in, s_e, s_gate);
 }
 
 // dA_log and ddt_bias: the tiles' sums, 16 strands of tiles per channel, in 64 bits
@@ -464,13 +535,6 @@ __global__ __launch_bounds__(1024) void linrec_sum_kernel(LinrecLaunch p) {
     (which ? p.ddt_bias : p.dA_log)[c] = (float)v;
 }
 
-// sequences without a token hand their state through: fwd ht = h0, bwd dh0 = dht
-__global__ __launch_bounds__(256) void linrec_empty_kernel(LinrecLaunch p, const float* from, float* to) {
-    const int64_t nb = (p.D + 255) / 256, n = blockIdx.x / nb, c = (blockIdx.x - n * nb) * 256 + threadIdx.x;
-    if (c >= p.D || (p.map.seqs ? p.map.seqs[n].y : p.map.T) > 0) return;
-    to[n * p.D + c] = from ? from[n * p.D + c] : 0.f;
-}
-
 // One token: y and the state, in place.
 template <typename X, typename G, bool ACT, bool NORM, int V>
 __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
@@ -480,9 +544,10 @@ __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
     Raw<X, V> x;
     Raw<G, V> g;
     Raw<float, V> h;
-    x.load(static_cast<const X*>(p.x) + n * p.xs + c);
-    g.load(static_cast<const G*>(p.g) + n * p.gs + c);
-    h.load(p.ht + n * p.D + c);
+    const unsigned ox = (unsigned)c * sizeof(X);
+    x.load(static_cast<const X*>(p.x) + n * p.xs, ox);
+    g.load(static_cast<const G*>(p.g) + n * p.gs, (unsigned)c * sizeof(G));
+    h.load(p.ht + n * p.D, (unsigned)c * 4);
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -490,8 +555,8 @@ __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
         const Gate q = gate_of<ACT, NORM, false>(g.get(e), rate2, bias);
         o[e] = q.a * h.get(e) + q.m * x.get(e);
     }
-    Raw<float, V>::store(p.ht + n * p.D + c, o);
-    Raw<X, V>::store(static_cast<X*>(p.y) + n * p.ys + c, o);
+    Raw<float, V>::store(p.ht + n * p.D, (unsigned)c * 4, o);
+    Raw<X, V>::store(static_cast<X*>(p.y) + n * p.ys, ox, o);
 }
 
 // ---- launches
@@ -534,39 +599,32 @@ static hipError_t go(const LinrecLaunch& p) {
     return two ? go0<WHICH, 2>(p) : go0<WHICH, 1>(p);
 }
 
-static hipError_t empty(const LinrecLaunch& p, const float* from, float* to) {
-    if (!to || (!p.map.seqs && p.map.T > 0)) return hipSuccess;
-    hipLaunchKernelGGL(linrec_empty_kernel, dim3((unsigned)((p.D + 255) / 256 * p.map.N)), dim3(256), 0, p.stream, p,
-                       from, to);
-    return hipGetLastError();
-}
-
-static hipError_t clear(const LinrecLaunch& p) {
-    if (!p.pairs) return hipSuccess;
-    hipLaunchKernelGGL(linrec_clear_kernel, dim3((unsigned)((p.D + 255) / 256 * p.map.max_tiles)), dim3(256), 0,
-                       p.stream, p);
+// in front of the tiles' kernel; from, to: the state that sequences without a token hand through
+static hipError_t clear(const LinrecLaunch& p, const float* from, float* to) {
+    const bool empties = to && (p.map.seqs || p.map.T == 0);
+    const int64_t rows = (p.pairs ? p.map.max_tiles : 0) + (empties ? p.map.N : 0);
+    if (rows == 0) return hipSuccess;
+    hipLaunchKernelGGL(linrec_clear_kernel, dim3((unsigned)((p.D + 511) / 512 * rows)), dim3(256), 0, p.stream, p, from,
+                       to);
     return hipGetLastError();
 }
 
 hipError_t launch_linrec_fwd(const LinrecLaunch& p) {
-    hipError_t e = empty(p, p.h0, p.ht);
+    hipError_t e = clear(p, p.h0, p.ht);
     if (e != hipSuccess || p.map.max_tiles == 0) return e;
-    if ((e = clear(p)) != hipSuccess) return e;
     return go<FWD>(p);
 }
 
 hipError_t launch_linrec_bwd(const LinrecLaunch& p) {
-    hipError_t e = empty(p, p.dht, p.dh0);
-    if (e != hipSuccess) return e;
-    if (p.map.max_tiles > 0) {
-        if (p.own_states) {   // the states entering the tiles were not kept
-            LinrecLaunch f = p;
-            f.y = nullptr;
-            f.ht = nullptr;
-            if ((e = clear(f)) != hipSuccess || (e = go<FWD>(f)) != hipSuccess) return e;
-        }
-        if ((e = clear(p)) != hipSuccess || (e = go<BWD>(p)) != hipSuccess) return e;
+    hipError_t e;
+    if (p.own_states && p.map.max_tiles > 0) {   // the states entering the tiles were not kept
+        LinrecLaunch f = p;
+        f.y = nullptr;
+        f.ht = nullptr;
+        if ((e = launch_linrec_fwd(f)) != hipSuccess) return e;
     }
+    if ((e = clear(p, p.dht, p.dh0)) != hipSuccess) return e;
+    if (p.map.max_tiles > 0 && (e = go<BWD>(p)) != hipSuccess) return e;
     if (!(p.act.flags & ACT_GATE)) return hipSuccess;
     hipLaunchKernelGGL(linrec_sum_kernel, dim3((unsigned)(2 * ((p.D + 63) / 64))), dim3(1024), 0, p.stream, p);
     return hipGetLastError();

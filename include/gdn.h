@@ -505,7 +505,7 @@ enum { GDN_LINREC_NORMALIZE = 1 };
 typedef struct gdn_linrec_desc {
     int64_t batch;      /* B; must be 1 when cu_seqlens is given */
     int64_t seq_len;    /* T: tokens per sequence, or all packed tokens */
-    int64_t channels;   /* D >= 1 */
+    int64_t channels;   /* D: 1 to 2^28 - 1 */
     int64_t num_seqs;   /* N packed sequences when cu_seqlens is given, else 0 */
     int64_t x_stride;   /* token strides of x, of g and of y / dy */
     int64_t g_stride;
