@@ -17,10 +17,13 @@ gdn_status api_ok();
 
 // Tiles of `tile` tokens that never cross a sequence.  Without packed offsets
 // tile c is tokens (c % nt) * tile .. of sequence c / nt; with them a table
-// built on the device gives (first token, count, sequence, tile of its
-// sequence), count 0 for unused rows.
+// built on the device has a row for each, all that a workgroup needs in one load.
+struct TileRow {
+    int row0, n, seq, j;   // first token, tokens (0: unused row), sequence, tile of its sequence
+    int nt, len, pad[2];   // tiles and tokens of the sequence
+};
 struct SeqMap {
-    const int4* table = nullptr;   // [max_tiles] or nullptr
+    const TileRow* table = nullptr;   // [max_tiles] or nullptr
     const int4* seqs = nullptr;    // [N] (first token, length, first tile, 0) or nullptr
     int64_t T = 0;                 // tokens per sequence when table == nullptr
     int64_t nt = 0;                // tiles per sequence when table == nullptr
@@ -34,6 +37,7 @@ struct Tile {
     int n;          // tokens; 0: unused
     int seq;
     int j, nt;      // tile j of the nt of its sequence
+    int len;        // tokens of the sequence
 };
 
 // c is the same for the whole wave, and so is what comes back: in scalar
@@ -41,12 +45,13 @@ struct Tile {
 __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
     Tile t;
     if (m.table) {
-        const int4 r = m.table[c];
-        t.row0 = __builtin_amdgcn_readfirstlane(r.x);
-        t.n = __builtin_amdgcn_readfirstlane(r.y);
-        t.seq = __builtin_amdgcn_readfirstlane(r.z);
-        t.j = __builtin_amdgcn_readfirstlane(r.w);
-        t.nt = t.n > 0 ? (__builtin_amdgcn_readfirstlane(m.seqs[t.seq].y) + m.tile - 1) / m.tile : 0;
+        const TileRow r = m.table[c];
+        t.row0 = __builtin_amdgcn_readfirstlane(r.row0);
+        t.n = __builtin_amdgcn_readfirstlane(r.n);
+        t.seq = __builtin_amdgcn_readfirstlane(r.seq);
+        t.j = __builtin_amdgcn_readfirstlane(r.j);
+        t.nt = __builtin_amdgcn_readfirstlane(r.nt);
+        t.len = __builtin_amdgcn_readfirstlane(r.len);
     } else {
         const unsigned nt = (unsigned)m.nt, b = (unsigned)c / nt;   // both below 2^31
         t.j = (int)((unsigned)c - b * nt);
@@ -55,6 +60,7 @@ __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
         t.row0 = b * m.T + at;
         t.n = (int)min((int64_t)m.tile, m.T - at);
         t.nt = (int)nt;
+        t.len = (int)m.T;
     }
     return t;
 }
@@ -64,7 +70,8 @@ struct TileTableLaunch {
     const int64_t* cu_seqlens;
     int64_t N, T, max_tiles;
     int tile;
-    int4 *table, *seqs;
+    TileRow* table;
+    int4* seqs;
     int* words;
     hipStream_t stream;
 };

@@ -56,7 +56,7 @@ TileLayout tile_layout(int64_t B, int64_t T, int64_t N, int tile) {
     L.tiles = N > 0 ? L.nt + N : B * L.nt;
     L.seqs = 256;
     L.table = L.seqs + align256(N > 0 ? (size_t)N * 16 : 0);
-    L.end = L.table + align256(N > 0 ? (size_t)L.tiles * 16 : 0);
+    L.end = L.table + align256(N > 0 ? (size_t)L.tiles * sizeof(gdn::TileRow) : 0);
     return L;
 }
 
@@ -70,7 +70,7 @@ gdn::SeqMap seq_map(const TileLayout& L, int64_t B, int64_t T, int64_t N, int ti
     m.tile = tile;
     if (N > 0) {
         m.seqs = reinterpret_cast<const int4*>(p + L.seqs);
-        m.table = reinterpret_cast<const int4*>(p + L.table);
+        m.table = reinterpret_cast<const gdn::TileRow*>(p + L.table);
     }
     return m;
 }
@@ -82,7 +82,7 @@ gdn_status make_table(const gdn::SeqMap& m, const int64_t* cu, void* ws, hipStre
     t.T = m.T;
     t.max_tiles = m.max_tiles;
     t.tile = m.tile;
-    t.table = const_cast<int4*>(m.table);
+    t.table = const_cast<gdn::TileRow*>(m.table);
     t.seqs = const_cast<int4*>(m.seqs);
     t.words = static_cast<int*>(ws);
     t.stream = st;

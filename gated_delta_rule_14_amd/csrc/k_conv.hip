@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvLaunch a) {
     }
     if (t.n > 0) {
         // tokens of the sequence from this tile's first on; of them the tile and W - 1 more
-        const int64_t len = a.map.seqs ? a.map.seqs[t.seq].y : a.map.T, p0 = (int64_t)t.j * a.map.tile;
+        const int64_t len = t.len, p0 = (int64_t)t.j * a.map.tile;
         const int left = (int)min(len - p0, (int64_t)t.n + W - 1), all = t.n + W - 1;
         const T* x = static_cast<const T*>(a.x) + t.row0 * a.xs + c;
         const T* dy = static_cast<const T*>(a.dy) + t.row0 * a.ys + c;

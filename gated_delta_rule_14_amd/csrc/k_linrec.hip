@@ -148,66 +148,84 @@ __device__ __forceinline__ void publish(uint64_t* p, float A, float H) {
     const unsigned a = A != A ? 0x7fc00000u : __float_as_uint(A);
     __hip_atomic_store(p, (uint64_t)__float_as_uint(H) << 32 | a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ uint64_t peek(const uint64_t* row, unsigned off) {
+    return __hip_atomic_load((const GDN_GLOBAL uint64_t*)((const GDN_GLOBAL char*)in_scalar(row) + off),
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Compose the pairs at p, p + step, ... (n of them) in that order onto (A, H).
-// `polls`: what is left of this thread's patience; 0 once a wait gave up.
-__device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, float* A, float* H, int* polls) {
-    for (int i = 0; i < n; i += 8) {
-        uint64_t v[8];
+// Compose the pairs of channel c in rows p, p + step, ... (n of them; p, step and n the same
+// for the whole wave) in that order onto (A, H), 8 loads in flight at once.  `polls`: what
+// is left of this thread's patience; 0 once a wait gave up.
+__device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, int64_t c, float* A, float* H,
+                                        int* polls) {
+    constexpr int U = GROUP / 2;
+    const unsigned off = (unsigned)c * 8;
+    for (int i = 0; i < n; i += U) {
+        uint64_t v[U];
+        bool missing;
+        do {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = i + k < n ? peek(p + (i + k) * step) : 0;
+            for (int k = 0; k < U; ++k) v[k] = peek(p + min(i + k, n - 1) * step, off);
+            missing = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (i + k >= n) break;
-            while ((unsigned)v[k] == ABSENT && *polls > 0) {
-                --*polls;
-                __builtin_amdgcn_s_sleep(1);
-                v[k] = peek(p + (i + k) * step);
-            }
-            const float a = __uint_as_float((unsigned)v[k]);
-            *H = a * *H + __uint_as_float((unsigned)(v[k] >> 32));
+            for (int k = 0; k < U; ++k) missing |= (unsigned)v[k] == ABSENT;
+            if (missing) __builtin_amdgcn_s_sleep(1);
+        } while (missing && --*polls > 0);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const bool past = i + k >= n;
+            const float a = past ? 1.f : __uint_as_float((unsigned)v[k]);
+            *H = a * *H + (past ? 0.f : __uint_as_float((unsigned)(v[k] >> 32)));
             *A *= a;
         }
     }
 }
 
-// The value entering tile j (of nt) of a sequence, for channel c, out of what
-// the tiles before it publish; `tile` its row in the workspace, dir = 1 for
-// tiles in the order of the tokens, -1 against it (j then counts from the
-// sequence's end).  (A, H): the tile's own pair, published here.  The first
-// tile's pair is published with the value `start` that enters the sequence
-// worked in, as is its group's: those are values, and replace what is composed so far.
-__device__ __forceinline__ float enter(const LinrecLaunch& p, int64_t tile, int j, int nt, int dir, int64_t c,
-                                       float A, float H, float start) {
-    uint64_t* const one = p.pairs + tile * p.D + c;
-    const bool followed = j + 1 < nt;
-    if (j == 0) {
-        if (followed) publish(one, 0.f, A * start + H);
-        return start;
-    }
-    if (followed) publish(one, A, H);
+// What enters tile j of a sequence (of nt; row `tile` of the workspace) is put
+// together from the pairs of the tiles and groups before it by NT threads to
+// a channel: two halves of its own group's tiles (parts 0, 1), two of the
+// groups before (parts 2, 3), all waited for at once.  dir = 1: tiles in the
+// order of the tokens; -1: against it, j counted from the sequence's end.
+// The first tile's pair, and its group's, are published as (0, value) with
+// the value that enters the sequence worked in: composing onto anything gives that value.
+constexpr int NT = 4;
+__device__ __forceinline__ void enter_part(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
+                                           float start, float* A, float* H) {
+    const int in = j % GROUP, ng = j / GROUP;
     int polls = POLLS;
-    const int ng = j / GROUP, in = j - ng * GROUP;
-    float v = 0.f, gA = 1.f, gH = 0.f;
-    if (ng > 0) {
-        // rows of the groups' last tiles: 16 tiles apart, so a sixteenth of the row is their own
-        const int64_t last0 = tile + (int64_t)dir * (GROUP - 1 - j);
-        for (int g = 0; g < ng; ++g) {
-            const uint64_t* q = p.groups + ((last0 + (int64_t)dir * g * GROUP) / GROUP) * p.D + c;
-            float a = 1.f, h = 0.f;
-            compose(q, 0, 1, &a, &h, &polls);
-            v = g == 0 ? h : a * v + h;
-        }
+    *A = 1.f;
+    *H = 0.f;
+    if (part < 2) {
+        const int s0 = part * (GROUP / 2), n = min(in - s0, GROUP / 2);
+        compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
+        if (part == 0 && j == 0) *H = start;
+        if (part == 0 && j < GROUP) *A = 0.f;      // a value, whatever the A of the pairs after the first
+    } else {
+        // a group's row is a sixteenth of its last tile's, which no other group's is
+        const int64_t first = (tile + (int64_t)dir * (GROUP - 1 - j)) / GROUP;
+        const int half = (ng + 1) / 2, s0 = (part - 2) * half, n = min(ng - s0, half);
+        compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
+        if (part == 2 && ng > 0) *A = 0.f;
     }
-    compose(one - (int64_t)dir * in * p.D, (int64_t)dir * p.D, in, &gA, &gH, &polls);
-    if (in == GROUP - 1 && followed)
-        publish(p.groups + (tile / GROUP) * p.D + c, ng == 0 ? 0.f : gA * A, A * gH + H);
     if (polls == 0) atomicExch(p.words + 1, 1);
-    // without a group before, the first of the pairs above was the first tile's value (A = 0)
-    return ng == 0 ? gH : gA * v + gH;
+}
+// the tile's own pair; and once the parts of its group are there, the group's
+__device__ __forceinline__ void publish_tile(const LinrecLaunch& p, int64_t tile, int j, int nt, int64_t c, float A,
+                                             float H, float start) {
+    if (j + 1 < nt) publish(p.pairs + tile * p.D + c, j == 0 ? 0.f : A, j == 0 ? A * start + H : H);
+}
+template <int CB>
+__device__ __forceinline__ void publish_group(const LinrecLaunch& p, int64_t tile, int j, int nt, int64_t c, float A,
+                                              float H, const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
+    if (j % GROUP == GROUP - 1 && j + 1 < nt)
+        publish(p.groups + (tile / GROUP) * p.D + c, j < GROUP ? 0.f : s_pA[0][k] * s_pA[1][k] * A,
+                A * (s_pA[1][k] * s_pH[0][k] + s_pH[1][k]) + H);
+}
+template <int CB> __device__ __forceinline__ float entering(const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
+    float v = s_pH[2][k];
+    v = s_pA[3][k] * v + s_pH[3][k];
+    v = s_pA[0][k] * v + s_pH[0][k];
+    return s_pA[1][k] * v + s_pH[1][k];
 }
 
 // Every pair that some tile reads is marked absent, the ticket and the words
@@ -270,7 +288,8 @@ __device__ __forceinline__ const T* row_at(const T* tile, int64_t stride, const 
 
 template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
-                                         float (*s_A)[64 * V], float (*s_H)[64 * V], float* s_in) {
+                                         float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_pA)[64 * V],
+                                         float (*s_pH)[64 * V]) {
     constexpr int CB = 64 * V;
     const Spot s = spot_of<V, S>(p, t, c0);
     const X* x = static_cast<const X*>(p.x) + t.row0 * p.xs;
@@ -309,26 +328,37 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
     }
     __syncthreads();
     const int tid = threadIdx.x;
-    if (tid < CB && c0 + tid < p.D) {
-        const int64_t cc = c0 + tid;
-        float tA = 1.f, tH = 0.f;
+    const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
+    const bool own = part == 0 && c0 + k < p.D;
+    float tA = 1.f, tH = 0.f;
+    if (part < NT && c0 + k < p.D) {
+        const int64_t cc = c0 + k;
+        float start = 0.f, A, H;
+        if (part == 0) {
 #pragma unroll 4
-        for (int i = 0; i < NW; ++i) {
-            tH = s_A[i][tid] * tH + s_H[i][tid];
-            tA *= s_A[i][tid];
+            for (int i = 0; i < NW; ++i) {
+                tH = s_A[i][k] * tH + s_H[i][k];
+                tA *= s_A[i][k];
+            }
+            start = t.j == 0 && p.h0 ? p.h0[t.seq * p.D + cc] : 0.f;
+            publish_tile(p, tile, t.j, t.nt, cc, tA, tH, start);
         }
-        const float h0 = t.j == 0 && p.h0 ? p.h0[t.seq * p.D + cc] : 0.f;
-        const float in = t.nt > 1 ? enter(p, tile, t.j, t.nt, 1, cc, tA, tH, h0) : h0;
-        s_in[tid] = in;
-        if (p.states) p.states[tile * p.D + cc] = in;
-        if (p.ht && t.j + 1 == t.nt) p.ht[t.seq * p.D + cc] = tA * in + tH;
+        enter_part(p, tile, t.j, 1, cc, part, start, &A, &H);
+        s_pA[part][k] = A;
+        s_pH[part][k] = H;
+    }
+    __syncthreads();
+    if (own) {
+        publish_group<CB>(p, tile, t.j, t.nt, c0 + k, tA, tH, s_pA, s_pH, k);
+        const float in = entering<CB>(s_pA, s_pH, k);
+        if (p.states) p.states[tile * p.D + c0 + k] = in;
+        if (p.ht && t.j + 1 == t.nt) p.ht[t.seq * p.D + c0 + k] = tA * in + tH;
     }
     if (!p.y) return;
-    __syncthreads();
     float h[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        h[e] = s_in[s.lane * V + e];
+        h[e] = entering<CB>(s_pA, s_pH, s.lane * V + e);
         for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
     }
     if (!s.in) return;
@@ -342,17 +372,17 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
 }
 
 template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
-__global__ __launch_bounds__(64 * NW) void linrec_fwd_kernel(LinrecLaunch p) {
+__global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
-    static_assert(CB <= 64 * NW, "one thread per channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_in[CB];
+    static_assert(NT * CB <= 64 * NW, "NT threads to a channel of the block");
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[NT][CB], s_pH[NT][CB];
     __shared__ unsigned s_ticket;
     const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB), tile = k / nb;
     const int64_t c0 = (int64_t)(k - tile * nb) * CB;
     const Tile t = tile_of(p.map, tile);
     if (t.n <= 0) return;
-    if (t.n == S * NW) fwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_in);
-    else fwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_in);
+    if (t.n == S * NW) fwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
+    else fwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
 }
 
 // The same tiles taken from the last token: e = a (dy + e') is what a token
@@ -362,7 +392,8 @@ __global__ __launch_bounds__(64 * NW) void linrec_fwd_kernel(LinrecLaunch p) {
 template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_E)[64 * V],
-                                         float* s_in, float* s_e, f32x2v (*s_gate)[64 * NW]) {
+                                         float (*s_pA)[64 * V], float (*s_pE)[64 * V], float* s_in,
+                                         f32x2v (*s_gate)[64 * NW]) {
     constexpr int CB = 64 * V;
     const Spot s = spot_of<V, S>(p, t, c0);
     const int tid = threadIdx.x;
@@ -414,27 +445,37 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
         s_E[s.w][s.lane * V + e] = E[e];
     }
     __syncthreads();
-    if (tid < CB && c0 + tid < p.D) {
-        const int64_t cc = c0 + tid;
-        float tA = 1.f, tE = 0.f;
+    const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
+    const bool own = part == 0 && c0 + k < p.D;
+    const int back = t.nt - 1 - t.j;                           // the tile counted from the sequence's end
+    float tA = 1.f, tE = 0.f;
+    if (part < NT && c0 + k < p.D) {
+        const int64_t cc = c0 + k;
+        float start = 0.f, pA, pE;
+        if (part == 0) {
 #pragma unroll 2
-        for (int i = NW - 1; i >= 0; --i) {
-            tE = s_A[i][tid] * tE + s_E[i][tid];
-            tA *= s_A[i][tid];
+            for (int i = NW - 1; i >= 0; --i) {
+                tE = s_A[i][k] * tE + s_E[i][k];
+                tA *= s_A[i][k];
+            }
+            start = back == 0 && p.dht ? p.dht[t.seq * p.D + cc] : 0.f;
+            publish_tile(p, tile, back, t.nt, cc, tA, tE, start);
+            s_in[k] = p.states[tile * p.D + cc];
         }
-        const bool end = t.j + 1 == t.nt;
-        const float d0 = end && p.dht ? p.dht[t.seq * p.D + cc] : 0.f;
-        const float in = t.nt > 1 ? enter(p, tile, t.nt - 1 - t.j, t.nt, -1, cc, tA, tE, d0) : d0;
-        s_e[tid] = in;
-        s_in[tid] = p.states[tile * p.D + cc];
-        if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + cc] = tA * in + tE;
+        enter_part(p, tile, back, -1, cc, part, start, &pA, &pE);
+        s_pA[part][k] = pA;
+        s_pE[part][k] = pE;
     }
     __syncthreads();
+    if (own) {
+        publish_group<CB>(p, tile, back, t.nt, c0 + k, tA, tE, s_pA, s_pE, k);
+        if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + c0 + k] = tA * entering<CB>(s_pA, s_pE, k) + tE;
+    }
     float h[V], d[V], sA[V], sb[V], before[S][V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         h[e] = s_in[s.lane * V + e];
-        d[e] = s_e[s.lane * V + e];
+        d[e] = entering<CB>(s_pA, s_pE, s.lane * V + e);
         for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
         for (int i = NW - 1; i > s.w; --i) d[e] = s_A[i][s.lane * V + e] * d[e] + s_E[i][s.lane * V + e];
         sA[e] = 0.f;
@@ -498,8 +539,8 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
 template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
-    static_assert(CB <= 64 * NW, "one thread per channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB], s_in[CB], s_e[CB];
+    static_assert(NT * CB <= 64 * NW, "NT threads to a channel of the block");
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB], s_pA[NT][CB], s_pE[NT][CB], s_in[CB];
     // log2 a and sigmoid of every token, each thread's own: they are wanted again only at
     // the end, and next to a, m, x and dy there are no registers for them
     __shared__ f32x2v s_gate[ACT ? S * V : 1][64 * NW];
@@ -516,8 +557,8 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
         }
         return;
     }
-    if (t.n == S * NW) bwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_in, s_e, s_gate);
-    else bwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_in, s_e, s_gate);
+    if (t.n == S * NW) bwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
+    else bwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
 }
 
 // dA_log and ddt_bias: the tiles' sums, 16 strands of tiles per channel, in 64 bits

@@ -46,13 +46,12 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
         for (int i = wave; i < 1024 && base + i < a.N; i += 16) {
             const int4 q = s_seq[i];
             for (int64_t j = lane; j < q.w && q.z + j < a.max_tiles; j += 64)
-                a.table[q.z + j] = make_int4((int)(q.x + j * a.tile),
-                                             (int)min((int64_t)a.tile, q.y - j * a.tile),
-                                             (int)(base + i), (int)j);
+                a.table[q.z + j] = TileRow{(int)(q.x + j * a.tile), (int)min((int64_t)a.tile, q.y - j * a.tile),
+                                           (int)(base + i), (int)j, q.w, q.y, {0, 0}};
         }
         carry += total;
     }
-    for (int64_t c = carry + tid; c < a.max_tiles; c += 1024) a.table[c] = make_int4(0, 0, 0, 0);
+    for (int64_t c = carry + tid; c < a.max_tiles; c += 1024) a.table[c] = TileRow{};
     __syncthreads();   // every thread's check of the offsets is in s_bad
     if (tid == 0) {
         a.words[0] = s_bad;
