@@ -15,6 +15,22 @@ namespace gdn {
 gdn_status api_fail(gdn_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 gdn_status api_ok();
 
+// A row's address, held in scalar registers (the row is the same for the whole
+// wave, the channel a 32-bit byte offset of it): left to itself the compiler
+// adds the channel to the tensor's base first, and every row then costs a
+// 64-bit vector addition and two vector registers while its load is in flight.
+#define GDN_GLOBAL __attribute__((address_space(1)))
+template <typename T> __device__ __forceinline__ T* in_scalar(T* row) {
+    asm("" : "+s"(row));
+    return row;
+}
+template <typename U> __device__ __forceinline__ U peek_row(const void* row, unsigned off) {
+    return *(const GDN_GLOBAL U*)((const GDN_GLOBAL char*)row + off);
+}
+template <typename U> __device__ __forceinline__ void poke_row(void* row, unsigned off, U v) {
+    *(GDN_GLOBAL U*)((GDN_GLOBAL char*)row + off) = v;
+}
+
 // Tiles of `tile` tokens that never cross a sequence.  Without packed offsets
 // tile c is tokens (c % nt) * tile .. of sequence c / nt; with them a table
 // built on the device has a row for each, all that a workgroup needs in one load.
@@ -77,6 +93,21 @@ struct TileTableLaunch {
 };
 hipError_t launch_tile_table(const TileTableLaunch& a);
 
+// Gradients of parameters: the sums of `rows` partial rows [count][D], in a
+// fixed order and 64 bits.  Parts 0 .. W-1 of a row go to out0 [D][W] (W >= 1),
+// part W to out1 [D]; either may be nullptr.
+struct RowSumLaunch {
+    const float* part;
+    int64_t rows, D;
+    int W, count;
+    float *out0, *out1;
+    double* sums;                 // [shares][count][D], used where shares > 1
+    hipStream_t stream;
+    int64_t shares = 1;           // set by the launch
+};
+int64_t row_sum_shares(int64_t rows, int64_t cols);
+hipError_t launch_row_sum(const RowSumLaunch& a);
+
 struct LinrecLaunch {
     SeqMap map;
     Act act;                      // ACT_GATE: A_log, dt_bias [D]
@@ -88,6 +119,7 @@ struct LinrecLaunch {
     float* states = nullptr;      // [max_tiles][D] the states entering the tiles
     bool own_states = false;      // backward: states is workspace, to be filled first
     float* part = nullptr;        // [max_tiles][2][D] sums of dA_log and ddt_bias (backward)
+    double* sums = nullptr;       // shares of the sums of part
     // hand-offs between the tiles of a sequence; nullptr where every sequence is one tile
     uint64_t *pairs = nullptr, *groups = nullptr;   // [max_tiles][D], [max_tiles / 16 + 1][D]
     int* words = nullptr;         // check of the offsets, failed waits, ticket
@@ -107,6 +139,7 @@ struct QkLaunch {
     void *qo, *ko;                // forward: outputs; backward: dq, dk
     const void *dqo = nullptr, *dko = nullptr;
     float *dqw = nullptr, *dkw = nullptr, *part = nullptr;
+    double* sums = nullptr;       // shares of the sums of part
     int64_t tokens, T, Hq, Hk, qs, ks, qhs, khs;
     int64_t split = 1;            // waves to a token (forward)
     int D, R, norm;
@@ -114,7 +147,7 @@ struct QkLaunch {
     float eps, offset;
     hipStream_t stream;
 };
-int64_t qk_bwd_blocks(int64_t tokens);   // rows of part: [2][blocks][D]
+int64_t qk_bwd_blocks(int64_t tokens);   // rows of part [blocks][2][D]
 hipError_t launch_qk(const QkLaunch& a);
 hipError_t launch_qk_bwd(const QkLaunch& a);
 
@@ -123,7 +156,9 @@ struct ConvLaunch {
     const void *x = nullptr, *s0 = nullptr, *dy = nullptr, *dst = nullptr;
     const float *w = nullptr, *b = nullptr;
     void *y = nullptr, *st = nullptr, *dx = nullptr, *ds0 = nullptr;
-    float *dw = nullptr, *db = nullptr, *part = nullptr;
+    float *dw = nullptr, *db = nullptr;
+    float* part = nullptr;         // [tiles / 4, rounded up][W + 1][D] sums of dweight and dbias
+    double* sums = nullptr;        // shares of the sums of part
     int64_t D = 0, xs = 0, ys = 0;
     int W = 0;
     bool silu = false, bf16 = false;

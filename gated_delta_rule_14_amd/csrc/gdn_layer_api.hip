@@ -11,6 +11,11 @@ using gdn::api_ok;
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+// shares of the sums over `rows` partial rows of `cols`
+size_t sums_bytes(int64_t rows, int64_t cols) {
+    const int64_t n = gdn::row_sum_shares(rows, cols);
+    return n > 1 ? align256((size_t)(n * cols) * 8) : 0;
+}
 bool dtype_ok(int32_t t) { return t == GDN_DTYPE_F32 || t == GDN_DTYPE_BF16; }
 size_t size_of(int32_t t) { return t == GDN_DTYPE_BF16 ? 2 : 4; }
 gdn_status hip_fail(hipError_t e, const char* what) {
@@ -133,7 +138,7 @@ gdn_status check_linrec(const gdn_linrec_desc* d, const gdn_activation* act, gdn
 struct LinrecLayout {
     TileLayout t;
     bool hand_offs;
-    size_t pairs, groups, states, part, total;
+    size_t pairs, groups, states, part, sums, total;
 };
 LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
     LinrecLayout L;
@@ -149,6 +154,8 @@ LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
     if (backward) off += align256((size_t)L.t.tiles * D * 4);
     L.part = off;
     if (backward) off += align256((size_t)L.t.tiles * 2 * D * 4);
+    L.sums = off;
+    if (backward) off += sums_bytes(L.t.tiles, 2 * D);
     L.total = off;
     return L;
 }
@@ -157,7 +164,8 @@ LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
 gdn_status check_linrec_grid(const gdn_linrec_desc* d, const LinrecLayout& L) {
     const double D = (double)d->channels, N = (double)(d->num_seqs > 0 ? d->num_seqs : d->batch);
     gdn_status s = check_grid((double)L.t.tiles * ((D + 63) / 64), 1024);
-    return s != GDN_OK ? s : check_grid(N * ((D + 255) / 256), 256);
+    if (s == GDN_OK) s = check_grid((N + (double)L.t.tiles) * ((D + 511) / 512), 256);
+    return s != GDN_OK ? s : check_grid(2 * ((D + 15) / 16), 1024);
 }
 
 void linrec_place(gdn::LinrecLaunch* a, const gdn_linrec_desc* d, const LinrecLayout& L, void* workspace) {
@@ -275,7 +283,7 @@ gdn_status check_conv(const gdn_conv_desc* d, bool packed) {
 
 struct ConvLayout {
     TileLayout t;
-    size_t part, total;
+    size_t part, sums, total;
 };
 ConvLayout conv_layout(const gdn_conv_desc* d, bool backward) {
     ConvLayout L;
@@ -283,7 +291,9 @@ ConvLayout conv_layout(const gdn_conv_desc* d, bool backward) {
     // without packed offsets the forward needs no workspace
     size_t off = d->num_seqs > 0 || backward ? L.t.end : 0;
     L.part = off;
-    if (backward) off += align256((size_t)L.t.tiles * (d->width + 1) * d->channels * 4);
+    if (backward) off += align256((size_t)((L.t.tiles + 3) / 4) * (d->width + 1) * d->channels * 4);
+    L.sums = off;
+    if (backward) off += sums_bytes((L.t.tiles + 3) / 4, (d->width + 1) * d->channels);
     L.total = off;
     return L;
 }
@@ -305,11 +315,11 @@ gdn::ConvLaunch conv_launch(const gdn_conv_desc* d, const void* x, const float* 
     return a;
 }
 
-// the grids of the tiles, the empty sequences and the parameter sums
+// the grids of the tiles with the empty sequences, and of the parameter sums
 gdn_status check_conv_grid(const gdn::ConvLaunch& a) {
-    gdn_status s = check_grid((double)a.map.max_tiles * (double)((a.D + 63) / 64), 64);
-    if (s == GDN_OK) s = check_grid((double)a.map.N * (double)(((a.W - 1) * a.D + 255) / 256), 256);
-    return s != GDN_OK ? s : check_grid((double)(a.W + 1) * (double)((a.D + 63) / 64), 1024);
+    const double nb = (double)((a.D + 63) / 64);
+    const gdn_status s = check_grid(((double)a.map.max_tiles + (double)a.map.N + 8) * nb, 64);
+    return s != GDN_OK ? s : check_grid((a.W + 1) * nb, 1024);
 }
 
 }  // namespace
@@ -385,6 +395,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc* d, const gdn_activation* act_in
     a.own_states = !states;
     a.states = states ? const_cast<float*>(states) : reinterpret_cast<float*>(ws + L.states);
     a.part = reinterpret_cast<float*>(ws + L.part);
+    a.sums = reinterpret_cast<double*>(ws + L.sums);
     if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream)) != GDN_OK) return s;
     hipError_t e = gdn::launch_linrec_bwd(a);
     return e == hipSuccess ? api_ok() : hip_fail(e, "linear recurrence backward launch");
@@ -435,7 +446,8 @@ gdn_status gdn_qk_norm_rope_bwd_workspace(const gdn_qk_desc* d, size_t* bytes) {
     if (!bytes) return api_fail(GDN_ERR_NULL_ARG, "bytes is NULL");
     gdn_status s = check_qk(d);
     if (s != GDN_OK) return s;
-    *bytes = align256((size_t)gdn::qk_bwd_blocks(d->batch * d->seq_len) * 2 * d->head_dim * 4);
+    const int64_t blocks = gdn::qk_bwd_blocks(d->batch * d->seq_len);
+    *bytes = align256((size_t)blocks * 2 * d->head_dim * 4) + sums_bytes(blocks, 2 * d->head_dim);
     return api_ok();
 }
 
@@ -460,6 +472,8 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_desc* d, const void* q, const void*
     a.dqw = dq_weight;
     a.dkw = dk_weight;
     a.part = static_cast<float*>(workspace);
+    a.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) +
+                                       align256((size_t)gdn::qk_bwd_blocks(a.tokens) * 2 * a.D * 4));
     hipError_t e = gdn::launch_qk_bwd(a);
     return e == hipSuccess ? api_ok() : hip_fail(e, "q/k norm backward launch");
 }
@@ -524,6 +538,7 @@ gdn_status gdn_short_conv_bwd(const gdn_conv_desc* d, const void* x, const float
     a.db = dbias;
     a.ds0 = ds0;
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.part);
+    a.sums = reinterpret_cast<double*>(static_cast<char*>(workspace) + L.sums);
     if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream)) != GDN_OK) return s;
     hipError_t err = gdn::launch_conv_bwd(a);
     return err == hipSuccess ? api_ok() : hip_fail(err, "short convolution backward launch");

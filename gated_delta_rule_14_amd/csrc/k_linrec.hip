@@ -91,22 +91,7 @@ __device__ __forceinline__ Gate gate_of(float g, float rate2, float bias) {
     return r;
 }
 
-// ---- V consecutive elements as loaded, and their floats.  A row is the same
-// for the whole wave (a scalar base), the channel a 32-bit byte offset of it.
-// The row's address, held in scalar registers: left to itself the compiler adds
-// the channel to the tile's base first, and a row then costs a 64-bit vector
-// addition and two vector registers while its load is in flight.
-template <typename T> __device__ __forceinline__ T* in_scalar(T* row) {
-    asm("" : "+s"(row));
-    return row;
-}
-#define GDN_GLOBAL __attribute__((address_space(1)))
-template <typename U> __device__ __forceinline__ U peek_row(const void* row, unsigned off) {
-    return *(const GDN_GLOBAL U*)((const GDN_GLOBAL char*)row + off);
-}
-template <typename U> __device__ __forceinline__ void poke_row(void* row, unsigned off, U v) {
-    *(GDN_GLOBAL U*)((GDN_GLOBAL char*)row + off) = v;
-}
+// ---- V consecutive elements as loaded, and their floats
 template <typename T, int V> struct Raw;
 template <> struct Raw<bf16, 1> {
     uint32_t r;
@@ -561,21 +546,6 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     else bwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
 }
 
-// dA_log and ddt_bias: the tiles' sums, 16 strands of tiles per channel, in 64 bits
-__global__ __launch_bounds__(1024) void linrec_sum_kernel(LinrecLaunch p) {
-    __shared__ double s[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t nb = (p.D + 63) / 64, which = blockIdx.x / nb, c = (blockIdx.x - which * nb) * 64 + lane;
-    double v = 0;
-    if (c < p.D)
-        for (int64_t i = w; i < p.map.max_tiles; i += 16) v += p.part[(2 * i + which) * p.D + c];
-    s[w][lane] = v;
-    __syncthreads();
-    if (w != 0 || c >= p.D) return;
-    for (int i = 1; i < 16; ++i) v += s[i][lane];
-    (which ? p.ddt_bias : p.dA_log)[c] = (float)v;
-}
-
 // One token: y and the state, in place.
 template <typename X, typename G, bool ACT, bool NORM, int V>
 __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
@@ -667,8 +637,7 @@ hipError_t launch_linrec_bwd(const LinrecLaunch& p) {
     if ((e = clear(p, p.dht, p.dh0)) != hipSuccess) return e;
     if (p.map.max_tiles > 0 && (e = go<BWD>(p)) != hipSuccess) return e;
     if (!(p.act.flags & ACT_GATE)) return hipSuccess;
-    hipLaunchKernelGGL(linrec_sum_kernel, dim3((unsigned)(2 * ((p.D + 63) / 64))), dim3(1024), 0, p.stream, p);
-    return hipGetLastError();
+    return launch_row_sum(RowSumLaunch{p.part, p.map.max_tiles, p.D, 1, 2, p.dA_log, p.ddt_bias, p.sums, p.stream});
 }
 
 hipError_t launch_linrec_step(const LinrecLaunch& p) { return go<STEP>(p); }

@@ -256,26 +256,9 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkLaunch p) {
         if (e < p.D) {
             float s = 0.f;
             for (int i = 0; i < 4 * RPW; ++i) s += s_acc[i][e];
-            p.part[((int64_t)which * gridDim.x + blockIdx.x) * p.D + e] = s;
+            p.part[((int64_t)blockIdx.x * 2 + which) * p.D + e] = s;
         }
     }
-}
-
-// the workgroups' sums, 16 strands of workgroups per element, in 64 bits
-__global__ __launch_bounds__(1024) void qk_sum_kernel(QkLaunch p, int64_t blocks) {
-    __shared__ double s[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
-    const int64_t which = blockIdx.y;
-    float* out = which ? p.dkw : p.dqw;
-    if (!out) return;
-    double v = 0;
-    if (e < p.D)
-        for (int64_t i = w; i < blocks; i += 16) v += p.part[(which * blocks + i) * p.D + e];
-    s[w][lane] = v;
-    __syncthreads();
-    if (w != 0 || e >= p.D) return;
-    for (int i = 1; i < 16; ++i) v += s[i][lane];
-    out[e] = (float)v;
 }
 
 template <typename T, int LPR, bool INTER>
@@ -306,9 +289,12 @@ static hipError_t go(const QkLaunch& p, bool bwd) {
     return p.interleaved ? go1<float, true>(p, bwd) : go1<float, false>(p, bwd);
 }
 
-// Workgroups of the backward: two waves of tokens for every slot of the chip
-// at most, so that the sums over tokens stay in registers.
-int64_t qk_bwd_blocks(int64_t tokens) { return std::min((tokens + 3) / 4, (int64_t)2048); }
+// Workgroups of the backward: a token to a wave, more only to bound the partial
+// rows (16411 tokens of 40 heads: 119 us with one, 127 with two).
+int64_t qk_bwd_blocks(int64_t tokens) {
+    const int64_t per = std::max((int64_t)1, tokens / 16384);
+    return (tokens + 4 * per - 1) / (4 * per);
+}
 
 hipError_t launch_qk(const QkLaunch& p) { return go(p, false); }
 
@@ -318,9 +304,7 @@ hipError_t launch_qk_bwd(const QkLaunch& p) {
         if (e != hipSuccess) return e;
     }
     if (!p.dqw && !p.dkw) return hipSuccess;
-    hipLaunchKernelGGL(qk_sum_kernel, dim3((unsigned)((p.D + 63) / 64), 2), dim3(1024), 0, p.stream, p,
-                       qk_bwd_blocks(p.tokens));
-    return hipGetLastError();
+    return launch_row_sum(RowSumLaunch{p.part, qk_bwd_blocks(p.tokens), p.D, 1, 2, p.dqw, p.dkw, p.sums, p.stream});
 }
 
 }  // namespace gdn

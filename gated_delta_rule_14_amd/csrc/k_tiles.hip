@@ -1,4 +1,7 @@
-// The tile table of packed input for the layer operators: tiles of `tile`
+// What the layer operators share: the tile table of packed input, and the sums
+// of partial rows that make the gradients of parameters.
+//
+// The tile table: tiles of `tile`
 // tokens that restart at every sequence start, made on the device from the
 // caller's cu_seqlens.  Offsets are clamped into [0, T] (end >= start), so
 // invalid ones give wrong results but never an access out of bounds.
@@ -57,6 +60,65 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
         a.words[0] = s_bad;
         a.words[1] = 0;
     }
+}
+
+// A workgroup takes 64 columns and a share of the rows: 16 strands of rows to a
+// column, 8 loads of a strand in flight, met in LDS.  With many rows and few
+// columns the rows are shared out over a.shares workgroups and their sums
+// added by a second launch: one workgroup per 64 columns would leave most of
+// the chip idle (4103 rows of 256 columns: 28 us by 16 workgroups).
+template <bool LAST>
+__global__ __launch_bounds__(1024) void row_sum_kernel(RowSumLaunch a) {
+    __shared__ double s[16][64];
+    const int64_t cols = a.count * a.D;
+    const unsigned nb = (unsigned)((cols + 63) / 64), share = blockIdx.x / nb;
+    const int64_t col = (int64_t)(blockIdx.x - share * nb) * 64 + (threadIdx.x & 63);
+    const int strand = threadIdx.x >> 6;
+    double v = 0;
+    if (col < cols) {
+        if (LAST && a.shares > 1) {
+            for (int64_t i = strand; i < a.shares; i += 16) v += a.sums[i * cols + col];
+        } else {
+            const int64_t per = (a.rows + a.shares - 1) / a.shares, end = min(a.rows, (share + 1) * per);
+            const float* p = a.part + col;
+            for (int64_t i = share * per + strand; i < end; i += 8 * 16) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = i + k * 16 < end ? p[(i + k * 16) * cols] : 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v += x[k];
+            }
+        }
+    }
+    s[strand][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (strand != 0 || col >= cols) return;
+    for (int i = 1; i < 16; ++i) v += s[i][threadIdx.x];
+    if (!LAST) {
+        a.sums[share * cols + col] = v;
+        return;
+    }
+    const int64_t j = col / a.D, c = col - j * a.D;
+    if (j < a.W) {
+        if (a.out0) a.out0[c * a.W + j] = (float)v;
+    } else if (a.out1) {
+        a.out1[c] = (float)v;
+    }
+}
+
+int64_t row_sum_shares(int64_t rows, int64_t cols) { return cols < 8192 && rows > 512 ? 32 : 1; }
+
+hipError_t launch_row_sum(const RowSumLaunch& in) {
+    RowSumLaunch a = in;
+    const int64_t cols = a.count * a.D, nb = (cols + 63) / 64;
+    a.shares = row_sum_shares(a.rows, cols);
+    if (a.shares > 1) {
+        hipLaunchKernelGGL((row_sum_kernel<false>), dim3((unsigned)(nb * a.shares)), dim3(1024), 0, a.stream, a);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((row_sum_kernel<true>), dim3((unsigned)nb), dim3(1024), 0, a.stream, a);
+    return hipGetLastError();
 }
 
 hipError_t launch_tile_table(const TileTableLaunch& a) {
