@@ -7,17 +7,20 @@ the last one) has to be dense, and consecutive tokens evenly spaced."""
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
 from . import _binding as _b
-from ._binding import ACT_GATE, Activation, GdnError, _check, _debug, _dtype_code, _on
+from ._binding import ACT_GATE, Activation, GdnError, _check, _debug, _on
 
 _i64, _i32, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 LINREC_NORMALIZE = 1
 NORMS = {"none": 0, "l2": 1, "rms": 2}
 QK_INTERLEAVED = 1
 CONV_SILU = 1
+_CODES = {torch.float32: _b.DTYPE_F32, torch.bfloat16: _b.DTYPE_BF16}
+_F32 = torch.float32
 
 
 class LinrecDesc(ctypes.Structure):
@@ -40,17 +43,17 @@ class ConvDesc(ctypes.Structure):
 
 def declare(lib):
     """argtypes of the layer entry points (called by load())."""
-    P, Z = ctypes.c_void_p, ctypes.c_size_t
+    P, Z, Zp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
     L, Q, C, A = (ctypes.POINTER(t) for t in (LinrecDesc, QkDesc, ConvDesc, Activation))
     for name, args in (
-            ("gdn_linrec_workspace", [L, _i32, ctypes.POINTER(Z), ctypes.POINTER(_i64)]),
+            ("gdn_linrec_workspace", [L, _i32, Zp, ctypes.POINTER(_i64)]),
             ("gdn_linrec_fwd", [L, A] + [P] * 8 + [Z, P]),
             ("gdn_linrec_bwd", [L, A] + [P] * 13 + [Z, P]),
             ("gdn_linrec_step", [L, A] + [P] * 5),
             ("gdn_qk_norm_rope", [Q] + [P] * 9),
-            ("gdn_qk_norm_rope_bwd_workspace", [Q, ctypes.POINTER(Z)]),
+            ("gdn_qk_norm_rope_bwd_workspace", [Q, Zp]),
             ("gdn_qk_norm_rope_bwd", [Q] + [P] * 13 + [Z, P]),
-            ("gdn_short_conv_workspace", [C, _i32, ctypes.POINTER(Z)]),
+            ("gdn_short_conv_workspace", [C, _i32, Zp]),
             ("gdn_short_conv_fwd", [C] + [P] * 8 + [Z, P]),
             ("gdn_short_conv_bwd", [C] + [P] * 12 + [Z, P]),
             ("gdn_short_conv_step", [C] + [P] * 6)):
@@ -59,44 +62,54 @@ def declare(lib):
 
 
 # ---------------------------------------------------------------- arguments
+# A plan is what a call needs besides its tensors' addresses: the descriptor
+# and the workspace sizes of one set of shapes, strides and options.
+class _Plan:
+    __slots__ = ("desc", "at", "fwd", "bwd", "rows")
+
+    def __init__(self, desc):
+        self.desc, self.at = desc, ctypes.byref(desc)
+        self.fwd = self.bwd = self.rows = 0
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _same(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+def _code(t, name):
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    return c
 
 
-def _f32c(t, name, shape, dev):
-    """A dense float32 tensor of `shape` (None: absent)."""
-    if t is not None:
-        if t.dtype != torch.float32:
-            raise TypeError("%s must be torch.float32, got %s" % (name, t.dtype))
-        _dense(t, name, shape, dev)
-
-
-def _dense(t, name, shape, dev, dtype=None):
+def _dense(t, name, shape, dev, dtype=_F32):
+    """t is dense, of `shape` (a tuple) and `dtype`, on dev."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.device == dev:
+        return
     if t.device != dev:
         raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def _stride(t, name):
-    """Elements between the tokens of t [B, T, ...] ([N, ...]: one token each); 0 for dense rows."""
+    """Elements between the tokens of t [B, T, D] or [N, D] (one token each); 0 for dense rows."""
     if t.is_contiguous() or t.numel() == 0:
         return 0
-    B, T, s = t.shape[0], t.shape[1], t.stride()
-    inner = t[0, 0]
-    if inner.dim() == 1 and inner.numel() > 1 and s[-1] != 1:
+    s, D = t.stride(), t.shape[-1]
+    if D > 1 and s[-1] != 1:
         raise ValueError("%s must be dense in its last dimension" % name)
-    step = (s[0] if B > 1 else inner.numel()) if T == 1 else s[1]
-    if (B > 1 and T > 1 and s[0] != T * step) or (inner.dim() == 1 and step < inner.numel()):
-        raise ValueError("%s must hold evenly spaced tokens that do not overlap, got strides %s" % (name, s))
+    return _spacing(t.shape if t.dim() == 3 else (t.shape[0], 1), s, D, name)
+
+
+def _spacing(shape, s, width, name):
+    """The spacing of tokens [B, T] of `width` elements at strides s."""
+    B, T = shape[0], shape[1]
+    step = s[1] if T > 1 else s[0] if B > 1 else width
+    if (B > 1 and T > 1 and s[0] != T * step) or step < width:
+        raise ValueError("%s must hold evenly spaced tokens that do not overlap, got strides %s" % (name, tuple(s)))
     return step
 
 
@@ -110,21 +123,21 @@ def _run(fn, dev, stream, *args):
     """Call fn(*args, stream) with dev current; `stream` None: dev's current stream."""
     raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev.index:
-        _check(fn(*args, raw))
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, raw))
+            status = fn(*args, raw)
+    if status:
+        _check(status)
 
 
 def _workspace(ws, nbytes, dev):
     if nbytes == 0:
         return None, 0
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    else:
-        _same(dev, workspace=ws)
-        if not ws.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous on %s" % dev)
     return ws, ws.numel() * ws.element_size()
 
 
@@ -151,42 +164,51 @@ def _cu(cu, dev):
 
 
 # ------------------------------------------------- gated linear recurrence
-def _linrec(x, g, cu, normalize, A_log, dt_bias, y=None, lead=2):
-    dev = _device(x, "x")
-    if x.dim() != lead + 1 or g.shape != x.shape:
+@lru_cache(maxsize=1024)
+def _linrec_plan(B, T, D, N, xs, gs, ys, xd, gd, flags):
+    p = _Plan(LinrecDesc(B, T, D, N, xs, gs, ys, xd, gd, flags))
+    lib, n, rows = _b.load(), ctypes.c_size_t(), _i64()
+    _check(lib.gdn_linrec_workspace(p.at, 0, n, rows))
+    p.fwd, p.rows = n.value, rows.value
+    _check(lib.gdn_linrec_workspace(p.at, 1, n, None))
+    p.bwd = n.value
+    return p
+
+
+@lru_cache(maxsize=1024)
+def _linrec_step_plan(N, D, xs, gs, ys, xd, gd, flags):
+    return _Plan(LinrecDesc(N, 1, D, 0, xs, gs, ys, xd, gd, flags))
+
+
+def _linrec(x, g, normalize, A_log, dt_bias, y, dims):
+    """Checks shared by the entry points: the device, x's shape and what identifies a plan."""
+    dev, sh = _device(x, "x"), x.shape
+    if len(sh) != dims or g.shape != sh:
         raise ValueError("x and g must have one shape %s, got %s and %s"
-                         % ("[N, D]" if lead == 1 else "[B, T, D]", tuple(x.shape), tuple(g.shape)))
+                         % ("[N, D]" if dims == 2 else "[B, T, D]", tuple(sh), tuple(g.shape)))
     if g.device != dev:
         raise ValueError("g must be on %s" % dev)
-    if y is not None and (y.shape != x.shape or y.dtype != x.dtype or y.device != dev):
+    if y is not None and (y.shape != sh or y.dtype != x.dtype or y.device != dev):
         raise ValueError("y / dy must have the shape, type and device of x")
-    D = x.shape[-1]
-    if (A_log is None) != (dt_bias is None):
+    act = None
+    if A_log is not None and dt_bias is not None:
+        D = (sh[-1],)
+        _dense(A_log, "A_log", D, dev)
+        _dense(dt_bias, "dt_bias", D, dev)
+        act = ctypes.byref(Activation(ACT_GATE, A_log.data_ptr(), dt_bias.data_ptr()))
+    elif A_log is not None or dt_bias is not None:
         raise ValueError("A_log and dt_bias come together")
-    _f32c(A_log, "A_log", (D,), dev)
-    _f32c(dt_bias, "dt_bias", (D,), dev)
-    N = _cu(cu, dev)
-    if lead == 1:
-        x, g, y = x.unsqueeze(1), g.unsqueeze(1), None if y is None else y.unsqueeze(1)
-    d = LinrecDesc(x.shape[0], x.shape[1], D, N, _stride(x, "x"), _stride(g, "g"),
-                   0 if y is None else _stride(y, "y / dy"), _dtype_code(x), _dtype_code(g),
-                   LINREC_NORMALIZE if normalize else 0)
-    act = None if A_log is None else Activation(ACT_GATE, A_log.data_ptr(), dt_bias.data_ptr())
-    return d, act, dev, N or x.shape[0]
-
-
-def _linrec_sizes(d, backward):
-    lib = _b.load()
-    n, rows = ctypes.c_size_t(), _i64()
-    _check(lib.gdn_linrec_workspace(d, backward, n, rows))
-    return n.value, rows.value
+    key = (_stride(x, "x"), _stride(g, "g"), 0 if y is None else _stride(y, "y / dy"), _code(x, "x"), _code(g, "g"),
+           LINREC_NORMALIZE if normalize else 0)
+    return dev, sh, act, key
 
 
 def linrec_states(x, cu_seqlens=None):
     """A buffer for linrec_fwd's `states` (of x [B, T, D]), to be kept for linrec_bwd."""
     dev = _device(x, "x")
-    d = LinrecDesc(x.shape[0], x.shape[1], x.shape[2], _cu(cu_seqlens, dev), 0, 0, 0, 0, 0, 0)
-    return torch.empty((_linrec_sizes(d, 0)[1], x.shape[2]), dtype=torch.float32, device=dev)
+    B, T, D = x.shape
+    p = _linrec_plan(B, T, D, _cu(cu_seqlens, dev), 0, 0, 0, 0, 0, 0)
+    return torch.empty((p.rows, D), dtype=_F32, device=dev)
 
 
 def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_bias=None,
@@ -198,30 +220,37 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_b
     output_final_state).  `states`, from linrec_states(), is filled for
     linrec_bwd."""
     lib = _b.load()
-    d, act, dev, N = _linrec(x, g, cu_seqlens, normalize, A_log, dt_bias, y)
-    D = x.shape[2]
-    _f32c(h0, "h0", (N, D), dev)
-    _f32c(ht, "ht", (N, D), dev)
-    nbytes, rows = _linrec_sizes(d, 0)
-    _f32c(states, "states", (rows, D), dev)
+    dev, sh, act, key = _linrec(x, g, normalize, A_log, dt_bias, y, 3)
+    packed = _cu(cu_seqlens, dev)
+    p = _linrec_plan(*sh, packed, *key)
+    ends = (packed or sh[0], sh[2])
+    if h0 is not None:
+        _dense(h0, "h0", ends, dev)
+    if ht is not None:
+        _dense(ht, "ht", ends, dev)
+    if states is not None:
+        _dense(states, "states", (p.rows, sh[2]), dev)
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if output_final_state and ht is None:
-            ht = torch.empty((N, D), dtype=torch.float32, device=dev)
-        workspace, have = _workspace(workspace, nbytes, dev)
-    ht = ht if output_final_state else None
-    _run(lib.gdn_linrec_fwd, dev, stream, d, act, _p(x), _p(g), _p(h0), _p(cu_seqlens), _p(y), _p(ht),
-         _p(states), _p(workspace), have)
-    _words(workspace, dev, stream, cu_seqlens is not None, rows > N)
+            y = torch.empty(sh, dtype=x.dtype, device=dev)
+        if not output_final_state:
+            ht = None
+        elif ht is None:
+            ht = torch.empty(ends, dtype=_F32, device=dev)
+        workspace, have = _workspace(workspace, p.fwd, dev)
+    _run(lib.gdn_linrec_fwd, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(), _p(h0),
+         _p(cu_seqlens), y.data_ptr(), _p(ht), _p(states), _p(workspace), have)
+    _words(workspace, dev, stream, packed, p.rows > ends[0])
     return y, ht
 
 
 def _out(out, name, shape, dtype, dev):
-    if out.get(name) is None:
-        out[name] = torch.empty(shape, dtype=dtype, device=dev)
+    t = out.get(name)
+    if t is None:
+        out[name] = t = torch.empty(shape, dtype=dtype, device=dev)
     else:
-        _dense(out[name], name, shape, dev, dtype)
+        _dense(t, name, shape, dev, dtype)
+    return t.data_ptr()
 
 
 def linrec_bwd(x, g, dy, h0=None, dht=None, cu_seqlens=None, normalize=False, A_log=None, dt_bias=None,
@@ -231,28 +260,28 @@ def linrec_bwd(x, g, dy, h0=None, dht=None, cu_seqlens=None, normalize=False, A_
     A_log, dA_log and ddt_bias [D], float32.  `states` as linrec_fwd filled
     it for the same inputs (None: recomputed); `out` may supply outputs."""
     lib = _b.load()
-    d, act, dev, N = _linrec(x, g, cu_seqlens, normalize, A_log, dt_bias, dy)
-    D = x.shape[2]
-    _f32c(h0, "h0", (N, D), dev)
-    _f32c(dht, "dht", (N, D), dev)
-    _f32c(states, "states", (_linrec_sizes(d, 0)[1], D), dev)
-    nbytes, rows = _linrec_sizes(d, 1)
+    dev, sh, act, key = _linrec(x, g, normalize, A_log, dt_bias, dy, 3)
+    packed = _cu(cu_seqlens, dev)
+    p = _linrec_plan(*sh, packed, *key)
+    ends, D = (packed or sh[0], sh[2]), (sh[2],)
+    if h0 is not None:
+        _dense(h0, "h0", ends, dev)
+    if dht is not None:
+        _dense(dht, "dht", ends, dev)
+    if states is not None:
+        _dense(states, "states", (p.rows, sh[2]), dev)
     out = dict(out or {})
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
-        _out(out, "dx", x.shape, x.dtype, dev)
-        _out(out, "dg", g.shape, g.dtype, dev)
-        if want_dh0:
-            _out(out, "dh0", (N, D), torch.float32, dev)
-        else:
+        dx, dg = _out(out, "dx", sh, x.dtype, dev), _out(out, "dg", sh, g.dtype, dev)
+        if not want_dh0:
             out["dh0"] = None
-        if act is not None:
-            _out(out, "dA_log", (D,), torch.float32, dev)
-            _out(out, "ddt_bias", (D,), torch.float32, dev)
-        workspace, have = _workspace(workspace, nbytes, dev)
-    _run(lib.gdn_linrec_bwd, dev, stream, d, act, _p(x), _p(g), _p(h0), _p(cu_seqlens), _p(dy), _p(dht),
-         _p(states), _p(out["dx"]), _p(out["dg"]), _p(out["dh0"]), _p(out.get("dA_log")) if act else None,
-         _p(out.get("ddt_bias")) if act else None, _p(workspace), have)
-    _words(workspace, dev, stream, cu_seqlens is not None, rows > N)
+        dh0 = _out(out, "dh0", ends, _F32, dev) if want_dh0 else None
+        dA = _out(out, "dA_log", D, _F32, dev) if act else None
+        db = _out(out, "ddt_bias", D, _F32, dev) if act else None
+        workspace, have = _workspace(workspace, p.bwd, dev)
+    _run(lib.gdn_linrec_bwd, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(), _p(h0),
+         _p(cu_seqlens), dy.data_ptr(), _p(dht), _p(states), dx, dg, dh0, dA, db, _p(workspace), have)
+    _words(workspace, dev, stream, packed, p.rows > ends[0])
     return out
 
 
@@ -260,52 +289,66 @@ def linrec_step(x, g, state, normalize=False, A_log=None, dt_bias=None, y=None, 
     """gdn_linrec_step: one token of N sequences, x and g [N, D]; state [N, D]
     float32 is updated in place.  Returns y [N, D], the new state in x's type."""
     lib = _b.load()
-    d, act, dev, N = _linrec(x, g, None, normalize, A_log, dt_bias, y, lead=1)
-    _f32c(state, "state", (N, x.shape[1]), dev)
+    dev, sh, act, key = _linrec(x, g, normalize, A_log, dt_bias, y, 2)
     if state is None:
         raise ValueError("state is required")
+    _dense(state, "state", sh, dev)
+    p = _linrec_step_plan(*sh, *key)
     if y is None:
-        with _on(stream):
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _run(lib.gdn_linrec_step, dev, stream, d, act, _p(x), _p(g), _p(state), _p(y))
+        with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
+            y = torch.empty(sh, dtype=x.dtype, device=dev)
+    _run(lib.gdn_linrec_step, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(),
+         state.data_ptr(), y.data_ptr())
     return y
 
 
 # ------------------------------------------------------ q/k norm + rotation
+@lru_cache(maxsize=1024)
+def _qk_plan(*fields):
+    p = _Plan(QkDesc(*fields))
+    n = ctypes.c_size_t()
+    _check(_b.load().gdn_qk_norm_rope_bwd_workspace(p.at, n))
+    p.bwd = n.value
+    return p
+
+
 def _heads(t, name):
     """(token stride, head stride) of t [B, T, H, D]; (0, 0) when dense."""
     if t.is_contiguous() or t.numel() == 0:
         return 0, 0
-    H, D, s = t.shape[2], t.shape[3], t.stride()
+    sh, s = t.shape, t.stride()
+    H, D = sh[2], sh[3]
     if D > 1 and s[3] != 1:
         raise ValueError("%s must be dense in its last dimension" % name)
     hs = s[2] if H > 1 else D
-    step = _stride(t, name)
-    if t.shape[0] * t.shape[1] == 1:
-        step = max(step, (H - 1) * hs + D)
-    return step, hs
+    if hs < D:
+        raise ValueError("%s must hold heads that do not overlap, got strides %s" % (name, tuple(s)))
+    return _spacing(sh, s, (H - 1) * hs + D, name), hs
 
 
 def _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset, interleaved):
-    dev = _device(q, "q")
-    if q.dim() != 4 or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
-        raise ValueError("q [B, T, Hq, D] and k [B, T, Hk, D] do not match: %s, %s" % (tuple(q.shape), tuple(k.shape)))
+    dev, qs, ks = _device(q, "q"), q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or ks[:2] != qs[:2] or ks[3] != qs[3]:
+        raise ValueError("q [B, T, Hq, D] and k [B, T, Hk, D] do not match: %s, %s" % (tuple(qs), tuple(ks)))
     if k.dtype != q.dtype or k.device != dev:
         raise ValueError("k must have the type and device of q")
     if norm not in NORMS:
         raise ValueError("norm must be one of %s" % sorted(NORMS))
-    B, T, Hq, D = q.shape
+    B, T, Hq, D = qs
     R = 0
     if inv_freq is not None:
-        R = 2 * inv_freq.numel()
-        _dense(inv_freq, "inv_freq", (R // 2,), dev, torch.float64)
+        n = inv_freq.numel()
+        _dense(inv_freq, "inv_freq", (n,), dev, torch.float64)
+        R = 2 * n
     if positions is not None:
         _dense(positions, "positions", (B, T), dev, torch.int64)
-    _f32c(q_weight, "q_weight", (D,), dev)
-    _f32c(k_weight, "k_weight", (D,), dev)
-    (qs, qh), (ks, kh) = _heads(q, "q"), _heads(k, "k")
-    return QkDesc(B, T, Hq, k.shape[2], D, R, qs, ks, qh, kh, _dtype_code(q), NORMS[norm],
-                  QK_INTERLEAVED if interleaved else 0, eps, weight_offset), dev
+    if q_weight is not None:
+        _dense(q_weight, "q_weight", (D,), dev)
+    if k_weight is not None:
+        _dense(k_weight, "k_weight", (D,), dev)
+    (qt, qh), (kt, kh) = _heads(q, "q"), _heads(k, "k")
+    return _qk_plan(B, T, Hq, ks[2], D, R, qt, kt, qh, kh, _code(q, "q"), NORMS[norm],
+                    QK_INTERLEAVED if interleaved else 0, eps, weight_offset), dev, qs, ks
 
 
 def qk_norm_rope(q, k, inv_freq=None, positions=None, norm="l2", eps=1e-6, q_weight=None, k_weight=None,
@@ -317,18 +360,18 @@ def qk_norm_rope(q, k, inv_freq=None, positions=None, norm="l2", eps=1e-6, q_wei
     int64 (None: t).  q and k may be slices of one projection; returns dense
     (q_out, k_out), which chunk_fwd takes as they are."""
     lib = _b.load()
-    d, dev = _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset, interleaved)
+    p, dev, qs, ks = _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset, interleaved)
     with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = torch.empty(qs, dtype=q.dtype, device=dev)
         else:
-            _dense(q_out, "q_out", q.shape, dev, q.dtype)
+            _dense(q_out, "q_out", qs, dev, q.dtype)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            k_out = torch.empty(ks, dtype=k.dtype, device=dev)
         else:
-            _dense(k_out, "k_out", k.shape, dev, k.dtype)
-    _run(lib.gdn_qk_norm_rope, dev, stream, d, _p(q), _p(k), _p(q_weight), _p(k_weight), _p(inv_freq),
-         _p(positions), _p(q_out), _p(k_out))
+            _dense(k_out, "k_out", ks, dev, k.dtype)
+    _run(lib.gdn_qk_norm_rope, dev, stream, p.at, q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight),
+         _p(inv_freq), _p(positions), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -339,51 +382,51 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, inv_freq=None, positions=None, norm="
     Returns a dict dq, dk (dense, q's type) and, for each weight given,
     dq_weight, dk_weight [D] float32.  `out` may supply outputs."""
     lib = _b.load()
-    d, dev = _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset, interleaved)
-    _dense(dq_out, "dq_out", q.shape, dev, q.dtype)
-    _dense(dk_out, "dk_out", k.shape, dev, q.dtype)
-    n = ctypes.c_size_t()
-    _check(lib.gdn_qk_norm_rope_bwd_workspace(d, n))
-    out = dict(out or {})
+    p, dev, qs, ks = _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset, interleaved)
+    _dense(dq_out, "dq_out", qs, dev, q.dtype)
+    _dense(dk_out, "dk_out", ks, dev, q.dtype)
+    out, D = dict(out or {}), (qs[3],)
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
-        _out(out, "dq", q.shape, q.dtype, dev)
-        _out(out, "dk", k.shape, q.dtype, dev)
-        for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
-            if w is not None:
-                _out(out, name, (q.shape[3],), torch.float32, dev)
-        need = n.value if q_weight is not None or k_weight is not None else 0
-        workspace, have = _workspace(workspace, need, dev)
-    _run(lib.gdn_qk_norm_rope_bwd, dev, stream, d, _p(q), _p(k), _p(q_weight), _p(k_weight), _p(inv_freq),
-         _p(positions), _p(dq_out), _p(dk_out), _p(out["dq"]), _p(out["dk"]),
-         _p(out["dq_weight"]) if q_weight is not None else None,
-         _p(out["dk_weight"]) if k_weight is not None else None, _p(workspace), have)
+        dq, dk = _out(out, "dq", qs, q.dtype, dev), _out(out, "dk", ks, q.dtype, dev)
+        dqw = _out(out, "dq_weight", D, _F32, dev) if q_weight is not None else None
+        dkw = _out(out, "dk_weight", D, _F32, dev) if k_weight is not None else None
+        workspace, have = _workspace(workspace, p.bwd if dqw or dkw else 0, dev)
+    _run(lib.gdn_qk_norm_rope_bwd, dev, stream, p.at, q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight),
+         _p(inv_freq), _p(positions), dq_out.data_ptr(), dk_out.data_ptr(), dq, dk, dqw, dkw, _p(workspace), have)
     return out
 
 
 # -------------------------------------------------------- short convolution
-def _conv(x, weight, bias, cu, silu, y=None, lead=2):
-    dev = _device(x, "x")
-    if x.dim() != lead + 1:
-        raise ValueError("x must be %s, got %s" % ("[N, D]" if lead == 1 else "[B, T, D]", tuple(x.shape)))
-    D = x.shape[-1]
-    if weight.dim() != 2:
-        raise ValueError("weight must be [D, W], got %s" % (tuple(weight.shape),))
-    _f32c(weight, "weight", (D, weight.shape[1]), dev)
-    _f32c(bias, "bias", (D,), dev)
-    if y is not None and (y.shape != x.shape or y.dtype != x.dtype or y.device != dev):
+@lru_cache(maxsize=1024)
+def _conv_plan(B, T, D, N, xs, ys, code, W, flags):
+    p = _Plan(ConvDesc(B, T, D, N, xs, ys, code, W, flags))
+    lib, n = _b.load(), ctypes.c_size_t()
+    _check(lib.gdn_short_conv_workspace(p.at, 0, n))
+    p.fwd = n.value
+    _check(lib.gdn_short_conv_workspace(p.at, 1, n))
+    p.bwd = n.value
+    return p
+
+
+@lru_cache(maxsize=1024)
+def _conv_step_plan(N, D, xs, ys, code, W, flags):
+    return _Plan(ConvDesc(N, 1, D, 0, xs, ys, code, W, flags))
+
+
+def _conv(x, weight, bias, silu, y, dims):
+    """Checks shared by the entry points: the device, x's shape and what identifies a plan."""
+    dev, sh, ws = _device(x, "x"), x.shape, weight.shape
+    if len(sh) != dims:
+        raise ValueError("x must be %s, got %s" % ("[N, D]" if dims == 2 else "[B, T, D]", tuple(sh)))
+    if len(ws) != 2:
+        raise ValueError("weight must be [D, W], got %s" % (tuple(ws),))
+    _dense(weight, "weight", (sh[-1], ws[1]), dev)
+    if bias is not None:
+        _dense(bias, "bias", (sh[-1],), dev)
+    if y is not None and (y.shape != sh or y.dtype != x.dtype or y.device != dev):
         raise ValueError("y / dy must have the shape, type and device of x")
-    N = _cu(cu, dev)
-    if lead == 1:
-        x, y = x.unsqueeze(1), None if y is None else y.unsqueeze(1)
-    return ConvDesc(x.shape[0], x.shape[1], D, N, _stride(x, "x"), 0 if y is None else _stride(y, "y / dy"),
-                    _dtype_code(x), weight.shape[1], CONV_SILU if silu else 0), dev, N or x.shape[0]
-
-
-def _conv_bytes(d, backward):
-    lib = _b.load()
-    n = ctypes.c_size_t()
-    _check(lib.gdn_short_conv_workspace(d, backward, n))
-    return n.value
+    return dev, sh, (_stride(x, "x"), 0 if y is None else _stride(y, "y / dy"), _code(x, "x"), ws[1],
+                     CONV_SILU if silu else 0)
 
 
 def short_conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, silu=True, output_final_state=False,
@@ -393,22 +436,25 @@ def short_conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, silu=True, ou
     type) are the inputs before each sequence.  Returns (y, st), st the last
     W - 1 inputs (None unless output_final_state)."""
     lib = _b.load()
-    d, dev, N = _conv(x, weight, bias, cu_seqlens, silu, y)
-    win = (N, d.width - 1, d.channels)
-    for t, name in ((s0, "s0"), (st, "st")):
-        if t is not None:
-            _dense(t, name, win, dev, x.dtype)
-    nbytes = _conv_bytes(d, 0)
+    dev, sh, key = _conv(x, weight, bias, silu, y, 3)
+    packed = _cu(cu_seqlens, dev)
+    p = _conv_plan(*sh, packed, *key)
+    win = (packed or sh[0], key[3] - 1, sh[2])
+    if s0 is not None:
+        _dense(s0, "s0", win, dev, x.dtype)
+    if st is not None:
+        _dense(st, "st", win, dev, x.dtype)
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if output_final_state and st is None:
+            y = torch.empty(sh, dtype=x.dtype, device=dev)
+        if not output_final_state:
+            st = None
+        elif st is None:
             st = torch.empty(win, dtype=x.dtype, device=dev)
-        workspace, have = _workspace(workspace, nbytes, dev)
-    st = st if output_final_state else None
-    _run(lib.gdn_short_conv_fwd, dev, stream, d, _p(x), _p(weight), _p(bias), _p(s0), _p(cu_seqlens), _p(y),
-         _p(st), _p(workspace), have)
-    _words(workspace, dev, stream, cu_seqlens is not None)
+        workspace, have = _workspace(workspace, p.fwd, dev)
+    _run(lib.gdn_short_conv_fwd, dev, stream, p.at, x.data_ptr(), weight.data_ptr(), _p(bias), _p(s0),
+         _p(cu_seqlens), y.data_ptr(), _p(st), _p(workspace), have)
+    _words(workspace, dev, stream, packed)
     return y, st
 
 
@@ -418,27 +464,26 @@ def short_conv_bwd(x, weight, dy, bias=None, s0=None, dst=None, cu_seqlens=None,
     Returns a dict dx, ds0 (x's type; ds0 None unless want_ds0), dweight and,
     with bias, dbias, float32.  `out` may supply outputs."""
     lib = _b.load()
-    d, dev, N = _conv(x, weight, bias, cu_seqlens, silu, dy)
-    win = (N, d.width - 1, d.channels)
-    for t, name in ((s0, "s0"), (dst, "dst")):
-        if t is not None:
-            _dense(t, name, win, dev, x.dtype)
-    nbytes = _conv_bytes(d, 1)
+    dev, sh, key = _conv(x, weight, bias, silu, dy, 3)
+    packed = _cu(cu_seqlens, dev)
+    p = _conv_plan(*sh, packed, *key)
+    win = (packed or sh[0], key[3] - 1, sh[2])
+    if s0 is not None:
+        _dense(s0, "s0", win, dev, x.dtype)
+    if dst is not None:
+        _dense(dst, "dst", win, dev, x.dtype)
     out = dict(out or {})
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
-        _out(out, "dx", x.shape, x.dtype, dev)
-        _out(out, "dweight", weight.shape, torch.float32, dev)
-        if bias is not None:
-            _out(out, "dbias", bias.shape, torch.float32, dev)
-        if want_ds0:
-            _out(out, "ds0", win, x.dtype, dev)
-        else:
+        dx = _out(out, "dx", sh, x.dtype, dev)
+        dw = _out(out, "dweight", weight.shape, _F32, dev)
+        db = _out(out, "dbias", bias.shape, _F32, dev) if bias is not None else None
+        if not want_ds0:
             out["ds0"] = None
-        workspace, have = _workspace(workspace, nbytes, dev)
-    _run(lib.gdn_short_conv_bwd, dev, stream, d, _p(x), _p(weight), _p(bias), _p(s0), _p(cu_seqlens), _p(dy),
-         _p(dst), _p(out["dx"]), _p(out["dweight"]), _p(out["dbias"]) if bias is not None else None,
-         _p(out["ds0"]), _p(workspace), have)
-    _words(workspace, dev, stream, cu_seqlens is not None)
+        ds0 = _out(out, "ds0", win, x.dtype, dev) if want_ds0 else None
+        workspace, have = _workspace(workspace, p.bwd, dev)
+    _run(lib.gdn_short_conv_bwd, dev, stream, p.at, x.data_ptr(), weight.data_ptr(), _p(bias), _p(s0),
+         _p(cu_seqlens), dy.data_ptr(), _p(dst), dx, dw, db, ds0, _p(workspace), have)
+    _words(workspace, dev, stream, packed)
     return out
 
 
@@ -446,10 +491,12 @@ def short_conv_step(x, weight, state, bias=None, silu=True, y=None, stream=None)
     """gdn_short_conv_step: one token of N sequences, x [N, D]; the window
     state [N, W - 1, D] (x's type) moves on in place.  Returns y [N, D]."""
     lib = _b.load()
-    d, dev, N = _conv(x, weight, bias, None, silu, y, lead=1)
-    _dense(state, "state", (N, d.width - 1, d.channels), dev, x.dtype)
+    dev, sh, key = _conv(x, weight, bias, silu, y, 2)
+    p = _conv_step_plan(*sh, *key)
+    _dense(state, "state", (sh[0], key[3] - 1, sh[1]), dev, x.dtype)
     if y is None:
-        with _on(stream):
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _run(lib.gdn_short_conv_step, dev, stream, d, _p(x), _p(weight), _p(bias), _p(state), _p(y))
+        with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
+            y = torch.empty(sh, dtype=x.dtype, device=dev)
+    _run(lib.gdn_short_conv_step, dev, stream, p.at, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(),
+         y.data_ptr())
     return y
