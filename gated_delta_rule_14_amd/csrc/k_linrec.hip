@@ -174,24 +174,29 @@ __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, 
 // The first tile's pair, and its group's, are published as (0, value) with
 // the value that enters the sequence worked in: composing onto anything gives that value.
 constexpr int NT = 4;
-__device__ __forceinline__ void enter_part(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
-                                           float start, float* A, float* H) {
-    const int in = j % GROUP, ng = j / GROUP;
+// part 0 or 1; start: the value that enters the sequence
+__device__ __forceinline__ void enter_own(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
+                                          float start, float* A, float* H) {
+    const int in = j % GROUP, s0 = part * (GROUP / 2), n = min(in - s0, GROUP / 2);
     int polls = POLLS;
     *A = 1.f;
     *H = 0.f;
-    if (part < 2) {
-        const int s0 = part * (GROUP / 2), n = min(in - s0, GROUP / 2);
-        compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
-        if (part == 0 && j == 0) *H = start;
-        if (part == 0 && j < GROUP) *A = 0.f;      // a value, whatever the A of the pairs after the first
-    } else {
-        // a group's row is a sixteenth of its last tile's, which no other group's is
-        const int64_t first = (tile + (int64_t)dir * (GROUP - 1 - j)) / GROUP;
-        const int half = (ng + 1) / 2, s0 = (part - 2) * half, n = min(ng - s0, half);
-        compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
-        if (part == 2 && ng > 0) *A = 0.f;
-    }
+    compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
+    if (part == 0 && j == 0) *H = start;
+    if (part == 0 && j < GROUP) *A = 0.f;          // a value, whatever the A of the pairs after the first
+    if (polls == 0) atomicExch(p.words + 1, 1);
+}
+// part 2 or 3
+__device__ __forceinline__ void enter_groups(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
+                                             float* A, float* H) {
+    // a group's row is a sixteenth of its last tile's, which no other group's is
+    const int64_t first = (tile + (int64_t)dir * (GROUP - 1 - j)) / GROUP;
+    const int ng = j / GROUP, half = (ng + 1) / 2, s0 = (part - 2) * half, n = min(ng - s0, half);
+    int polls = POLLS;
+    *A = 1.f;
+    *H = 0.f;
+    compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
+    if (part == 2 && ng > 0) *A = 0.f;
     if (polls == 0) atomicExch(p.words + 1, 1);
 }
 // the tile's own pair; and once the parts of its group are there, the group's
@@ -199,12 +204,13 @@ __device__ __forceinline__ void publish_tile(const LinrecLaunch& p, int64_t tile
                                              float H, float start) {
     if (j + 1 < nt) publish(p.pairs + tile * p.D + c, j == 0 ? 0.f : A, j == 0 ? A * start + H : H);
 }
+// (only of a group that has tiles behind it: closes_group)
+__device__ __forceinline__ bool closes_group(int j, int nt) { return j % GROUP == GROUP - 1 && j + 1 < nt; }
 template <int CB>
-__device__ __forceinline__ void publish_group(const LinrecLaunch& p, int64_t tile, int j, int nt, int64_t c, float A,
-                                              float H, const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
-    if (j % GROUP == GROUP - 1 && j + 1 < nt)
-        publish(p.groups + (tile / GROUP) * p.D + c, j < GROUP ? 0.f : s_pA[0][k] * s_pA[1][k] * A,
-                A * (s_pA[1][k] * s_pH[0][k] + s_pH[1][k]) + H);
+__device__ __forceinline__ void publish_group(const LinrecLaunch& p, int64_t tile, int j, int64_t c, float A, float H,
+                                              const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
+    publish(p.groups + (tile / GROUP) * p.D + c, j < GROUP ? 0.f : s_pA[0][k] * s_pA[1][k] * A,
+            A * (s_pA[1][k] * s_pH[0][k] + s_pH[1][k]) + H);
 }
 template <int CB> __device__ __forceinline__ float entering(const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
     float v = s_pH[2][k];
@@ -316,25 +322,26 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
     const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
     const bool own = part == 0 && c0 + k < p.D;
     float tA = 1.f, tH = 0.f;
-    if (part < NT && c0 + k < p.D) {
-        const int64_t cc = c0 + k;
-        float start = 0.f, A, H;
-        if (part == 0) {
+    const bool live = part < NT && c0 + k < p.D, closes = closes_group(t.j, t.nt);
+    if (own) {
 #pragma unroll 4
-            for (int i = 0; i < NW; ++i) {
-                tH = s_A[i][k] * tH + s_H[i][k];
-                tA *= s_A[i][k];
-            }
-            start = t.j == 0 && p.h0 ? p.h0[t.seq * p.D + cc] : 0.f;
-            publish_tile(p, tile, t.j, t.nt, cc, tA, tH, start);
+        for (int i = 0; i < NW; ++i) {
+            tH = s_A[i][k] * tH + s_H[i][k];
+            tA *= s_A[i][k];
         }
-        enter_part(p, tile, t.j, 1, cc, part, start, &A, &H);
-        s_pA[part][k] = A;
-        s_pH[part][k] = H;
     }
+    if (live && part < 2) {
+        const float start = t.j == 0 && part == 0 && p.h0 ? p.h0[t.seq * p.D + c0 + k] : 0.f;
+        if (part == 0) publish_tile(p, tile, t.j, t.nt, c0 + k, tA, tH, start);
+        enter_own(p, tile, t.j, 1, c0 + k, part, start, &s_pA[part][k], &s_pH[part][k]);
+    }
+    if (closes) {        // before waiting for other groups, or the groups would wait in a row
+        __syncthreads();
+        if (own) publish_group<CB>(p, tile, t.j, c0 + k, tA, tH, s_pA, s_pH, k);
+    }
+    if (live && part >= 2) enter_groups(p, tile, t.j, 1, c0 + k, part, &s_pA[part][k], &s_pH[part][k]);
     __syncthreads();
     if (own) {
-        publish_group<CB>(p, tile, t.j, t.nt, c0 + k, tA, tH, s_pA, s_pH, k);
         const float in = entering<CB>(s_pA, s_pH, k);
         if (p.states) p.states[tile * p.D + c0 + k] = in;
         if (p.ht && t.j + 1 == t.nt) p.ht[t.seq * p.D + c0 + k] = tA * in + tH;
@@ -434,26 +441,27 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
     const bool own = part == 0 && c0 + k < p.D;
     const int back = t.nt - 1 - t.j;                           // the tile counted from the sequence's end
     float tA = 1.f, tE = 0.f;
-    if (part < NT && c0 + k < p.D) {
-        const int64_t cc = c0 + k;
-        float start = 0.f, pA, pE;
-        if (part == 0) {
+    const bool live = part < NT && c0 + k < p.D, closes = closes_group(back, t.nt);
+    if (own) {
 #pragma unroll 2
-            for (int i = NW - 1; i >= 0; --i) {
-                tE = s_A[i][k] * tE + s_E[i][k];
-                tA *= s_A[i][k];
-            }
-            start = back == 0 && p.dht ? p.dht[t.seq * p.D + cc] : 0.f;
-            publish_tile(p, tile, back, t.nt, cc, tA, tE, start);
-            s_in[k] = p.states[tile * p.D + cc];
+        for (int i = NW - 1; i >= 0; --i) {
+            tE = s_A[i][k] * tE + s_E[i][k];
+            tA *= s_A[i][k];
         }
-        enter_part(p, tile, back, -1, cc, part, start, &pA, &pE);
-        s_pA[part][k] = pA;
-        s_pE[part][k] = pE;
+        s_in[k] = p.states[tile * p.D + c0 + k];
     }
+    if (live && part < 2) {
+        const float start = back == 0 && part == 0 && p.dht ? p.dht[t.seq * p.D + c0 + k] : 0.f;
+        if (part == 0) publish_tile(p, tile, back, t.nt, c0 + k, tA, tE, start);
+        enter_own(p, tile, back, -1, c0 + k, part, start, &s_pA[part][k], &s_pE[part][k]);
+    }
+    if (closes) {        // before waiting for other groups, or the groups would wait in a row
+        __syncthreads();
+        if (own) publish_group<CB>(p, tile, back, c0 + k, tA, tE, s_pA, s_pE, k);
+    }
+    if (live && part >= 2) enter_groups(p, tile, back, -1, c0 + k, part, &s_pA[part][k], &s_pE[part][k]);
     __syncthreads();
     if (own) {
-        publish_group<CB>(p, tile, back, t.nt, c0 + k, tA, tE, s_pA, s_pE, k);
         if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + c0 + k] = tA * entering<CB>(s_pA, s_pE, k) + tE;
     }
     float h[V], d[V], sA[V], sb[V], before[S][V];
