@@ -94,6 +94,13 @@ def _dense(t, name, shape, dev, dtype=_F32):
     raise ValueError("%s must be contiguous with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+# New outputs, on the device of a tensor at hand and without its values: an
+# allocation is a large part of a small call's time, and these forms of it take
+# 1.1 and 1.6 us where torch.empty with its arguments takes 2.1.
+def _like(t):
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _stride(t, name):
     """Elements between the tokens of t [B, T, D] or [N, D] (one token each); 0 for dense rows."""
     if t.is_contiguous() or t.numel() == 0:
@@ -131,11 +138,11 @@ def _run(fn, dev, stream, *args):
         _check(status)
 
 
-def _workspace(ws, nbytes, dev):
+def _workspace(ws, nbytes, dev, like):
     if nbytes == 0:
         return None, 0
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+        return like.new_empty(nbytes, dtype=torch.uint8), nbytes
     if ws.device != dev or not ws.is_contiguous():
         raise ValueError("workspace must be contiguous on %s" % dev)
     return ws, ws.numel() * ws.element_size()
@@ -208,7 +215,7 @@ def linrec_states(x, cu_seqlens=None):
     dev = _device(x, "x")
     B, T, D = x.shape
     p = _linrec_plan(B, T, D, _cu(cu_seqlens, dev), 0, 0, 0, 0, 0, 0)
-    return torch.empty((p.rows, D), dtype=_F32, device=dev)
+    return x.new_empty((p.rows, D), dtype=_F32)
 
 
 def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_bias=None,
@@ -232,22 +239,24 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_b
         _dense(states, "states", (p.rows, sh[2]), dev)
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
         if y is None:
-            y = torch.empty(sh, dtype=x.dtype, device=dev)
+            y = _like(x)
         if not output_final_state:
             ht = None
         elif ht is None:
-            ht = torch.empty(ends, dtype=_F32, device=dev)
-        workspace, have = _workspace(workspace, p.fwd, dev)
+            ht = x.new_empty(ends, dtype=_F32)
+        workspace, have = _workspace(workspace, p.fwd, dev, x)
     _run(lib.gdn_linrec_fwd, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(), _p(h0),
          _p(cu_seqlens), y.data_ptr(), _p(ht), _p(states), _p(workspace), have)
     _words(workspace, dev, stream, packed, p.rows > ends[0])
     return y, ht
 
 
-def _out(out, name, shape, dtype, dev):
+def _out(out, name, shape, dtype, dev, like):
+    """The address of output `name`: the one supplied, or a new one."""
     t = out.get(name)
     if t is None:
-        out[name] = t = torch.empty(shape, dtype=dtype, device=dev)
+        same = like.shape == shape and like.dtype is dtype
+        out[name] = t = _like(like) if same else like.new_empty(shape, dtype=dtype)
     else:
         _dense(t, name, shape, dev, dtype)
     return t.data_ptr()
@@ -272,13 +281,13 @@ def linrec_bwd(x, g, dy, h0=None, dht=None, cu_seqlens=None, normalize=False, A_
         _dense(states, "states", (p.rows, sh[2]), dev)
     out = dict(out or {})
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
-        dx, dg = _out(out, "dx", sh, x.dtype, dev), _out(out, "dg", sh, g.dtype, dev)
+        dx, dg = _out(out, "dx", sh, x.dtype, dev, x), _out(out, "dg", sh, g.dtype, dev, g)
         if not want_dh0:
             out["dh0"] = None
-        dh0 = _out(out, "dh0", ends, _F32, dev) if want_dh0 else None
-        dA = _out(out, "dA_log", D, _F32, dev) if act else None
-        db = _out(out, "ddt_bias", D, _F32, dev) if act else None
-        workspace, have = _workspace(workspace, p.bwd, dev)
+        dh0 = _out(out, "dh0", ends, _F32, dev, x if dht is None else dht) if want_dh0 else None
+        dA = _out(out, "dA_log", D, _F32, dev, A_log) if act else None
+        db = _out(out, "ddt_bias", D, _F32, dev, dt_bias) if act else None
+        workspace, have = _workspace(workspace, p.bwd, dev, x)
     _run(lib.gdn_linrec_bwd, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(), _p(h0),
          _p(cu_seqlens), dy.data_ptr(), _p(dht), _p(states), dx, dg, dh0, dA, db, _p(workspace), have)
     _words(workspace, dev, stream, packed, p.rows > ends[0])
@@ -296,7 +305,7 @@ def linrec_step(x, g, state, normalize=False, A_log=None, dt_bias=None, y=None, 
     p = _linrec_step_plan(*sh, *key)
     if y is None:
         with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
-            y = torch.empty(sh, dtype=x.dtype, device=dev)
+            y = _like(x)
     _run(lib.gdn_linrec_step, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(),
          state.data_ptr(), y.data_ptr())
     return y
@@ -363,11 +372,11 @@ def qk_norm_rope(q, k, inv_freq=None, positions=None, norm="l2", eps=1e-6, q_wei
     p, dev, qs, ks = _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset, interleaved)
     with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
         if q_out is None:
-            q_out = torch.empty(qs, dtype=q.dtype, device=dev)
+            q_out = _like(q)
         else:
             _dense(q_out, "q_out", qs, dev, q.dtype)
         if k_out is None:
-            k_out = torch.empty(ks, dtype=k.dtype, device=dev)
+            k_out = _like(k)
         else:
             _dense(k_out, "k_out", ks, dev, k.dtype)
     _run(lib.gdn_qk_norm_rope, dev, stream, p.at, q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight),
@@ -387,10 +396,10 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, inv_freq=None, positions=None, norm="
     _dense(dk_out, "dk_out", ks, dev, q.dtype)
     out, D = dict(out or {}), (qs[3],)
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
-        dq, dk = _out(out, "dq", qs, q.dtype, dev), _out(out, "dk", ks, q.dtype, dev)
-        dqw = _out(out, "dq_weight", D, _F32, dev) if q_weight is not None else None
-        dkw = _out(out, "dk_weight", D, _F32, dev) if k_weight is not None else None
-        workspace, have = _workspace(workspace, p.bwd if dqw or dkw else 0, dev)
+        dq, dk = _out(out, "dq", qs, q.dtype, dev, dq_out), _out(out, "dk", ks, q.dtype, dev, dk_out)
+        dqw = _out(out, "dq_weight", D, _F32, dev, q_weight) if q_weight is not None else None
+        dkw = _out(out, "dk_weight", D, _F32, dev, k_weight) if k_weight is not None else None
+        workspace, have = _workspace(workspace, p.bwd if dqw or dkw else 0, dev, q)
     _run(lib.gdn_qk_norm_rope_bwd, dev, stream, p.at, q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight),
          _p(inv_freq), _p(positions), dq_out.data_ptr(), dk_out.data_ptr(), dq, dk, dqw, dkw, _p(workspace), have)
     return out
@@ -446,12 +455,12 @@ def short_conv_fwd(x, weight, bias=None, s0=None, cu_seqlens=None, silu=True, ou
         _dense(st, "st", win, dev, x.dtype)
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
         if y is None:
-            y = torch.empty(sh, dtype=x.dtype, device=dev)
+            y = _like(x)
         if not output_final_state:
             st = None
         elif st is None:
-            st = torch.empty(win, dtype=x.dtype, device=dev)
-        workspace, have = _workspace(workspace, p.fwd, dev)
+            st = x.new_empty(win)
+        workspace, have = _workspace(workspace, p.fwd, dev, x)
     _run(lib.gdn_short_conv_fwd, dev, stream, p.at, x.data_ptr(), weight.data_ptr(), _p(bias), _p(s0),
          _p(cu_seqlens), y.data_ptr(), _p(st), _p(workspace), have)
     _words(workspace, dev, stream, packed)
@@ -474,13 +483,13 @@ def short_conv_bwd(x, weight, dy, bias=None, s0=None, dst=None, cu_seqlens=None,
         _dense(dst, "dst", win, dev, x.dtype)
     out = dict(out or {})
     with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
-        dx = _out(out, "dx", sh, x.dtype, dev)
-        dw = _out(out, "dweight", weight.shape, _F32, dev)
-        db = _out(out, "dbias", bias.shape, _F32, dev) if bias is not None else None
+        dx = _out(out, "dx", sh, x.dtype, dev, x)
+        dw = _out(out, "dweight", weight.shape, _F32, dev, weight)
+        db = _out(out, "dbias", bias.shape, _F32, dev, bias) if bias is not None else None
         if not want_ds0:
             out["ds0"] = None
-        ds0 = _out(out, "ds0", win, x.dtype, dev) if want_ds0 else None
-        workspace, have = _workspace(workspace, p.bwd, dev)
+        ds0 = _out(out, "ds0", win, x.dtype, dev, x if dst is None else dst) if want_ds0 else None
+        workspace, have = _workspace(workspace, p.bwd, dev, x)
     _run(lib.gdn_short_conv_bwd, dev, stream, p.at, x.data_ptr(), weight.data_ptr(), _p(bias), _p(s0),
          _p(cu_seqlens), dy.data_ptr(), _p(dst), dx, dw, db, ds0, _p(workspace), have)
     _words(workspace, dev, stream, packed)
@@ -496,7 +505,7 @@ def short_conv_step(x, weight, state, bias=None, silu=True, y=None, stream=None)
     _dense(state, "state", (sh[0], key[3] - 1, sh[1]), dev, x.dtype)
     if y is None:
         with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
-            y = torch.empty(sh, dtype=x.dtype, device=dev)
+            y = _like(x)
     _run(lib.gdn_short_conv_step, dev, stream, p.at, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(),
          y.data_ptr())
     return y
