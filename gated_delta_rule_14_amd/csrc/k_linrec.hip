@@ -23,7 +23,15 @@
 // wait for each other: every tile that one waits for belongs to a workgroup
 // that is already running and that publishes without a wait (a group's pair:
 // after waits of that kind), so every wait ends.  Each is bounded all the
-// same and reports in words[1].
+// same and reports in words[1], which ends the others' waits too.
+//
+// Measured (bf16 x and y): 4 x 4096 tokens of 2048 channels with fp32 gates 58 us,
+// 4.6 TB/s; 137 thousand packed tokens of 4096 channels with raw gates and
+// normalised inputs 0.70 ms, bound by the vector ALU (32 instructions and 3
+// transcendentals a token and channel, 0.63 ms of issue slots).  A tile is 128
+// tokens and 128 channels, 16 tokens to a wave: tiles of 64 tokens take 15 to
+// 35 % longer (a hand-off for half the work), of 256 leave one workgroup to a
+// CU, 8 % longer on the packed input.
 #include "gdn_layer.hpp"
 
 namespace gdn {
@@ -142,7 +150,7 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* row, unsigned off) {
 // for the whole wave) in that order onto (A, H), 8 loads in flight at once.  `polls`: what
 // is left of this thread's patience; 0 once a wait gave up.
 __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, int64_t c, float* A, float* H,
-                                        int* polls) {
+                                        int* polls, const int* failed) {
     constexpr int U = GROUP / 2;
     const unsigned off = (unsigned)c * 8;
     for (int i = 0; i < n; i += U) {
@@ -155,6 +163,9 @@ __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, 
 #pragma unroll
             for (int k = 0; k < U; ++k) missing |= (unsigned)v[k] == ABSENT;
             if (missing) __builtin_amdgcn_s_sleep(1);
+            // someone else's patience has run out: so has this thread's
+            if (missing && *polls % 1024 == 0 && __hip_atomic_load(failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+                *polls = 1;
         } while (missing && --*polls > 0);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -181,7 +192,7 @@ __device__ __forceinline__ void enter_own(const LinrecLaunch& p, int64_t tile, i
     int polls = POLLS;
     *A = 1.f;
     *H = 0.f;
-    compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
+    compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls, p.words + 1);
     if (part == 0 && j == 0) *H = start;
     if (part == 0 && j < GROUP) *A = 0.f;          // a value, whatever the A of the pairs after the first
     if (polls == 0) atomicExch(p.words + 1, 1);
@@ -195,7 +206,7 @@ __device__ __forceinline__ void enter_groups(const LinrecLaunch& p, int64_t tile
     int polls = POLLS;
     *A = 1.f;
     *H = 0.f;
-    compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls);
+    compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls, p.words + 1);
     if (part == 2 && ng > 0) *A = 0.f;
     if (polls == 0) atomicExch(p.words + 1, 1);
 }
@@ -380,7 +391,11 @@ __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) 
 // The same tiles taken from the last token: e = a (dy + e') is what a token
 // hands to the one before it, again a composition of affine maps, with the
 // same A.  The states before each token come from the state entering the
-// tile, kept by the forward.
+// tile, kept by the forward.  16 waves of 8 tokens: a, m, x, dy and the states
+// of 16 values a thread are what 128 registers hold.  2 x 8192 tokens of 2048
+// channels, bf16, raw gates, normalised: 116 us against 66 us of bytes and 73
+// us of ALU slots; one workgroup fills a CU, so the loads and the hand-off of
+// a tile are not hidden by another.
 template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_E)[64 * V],
@@ -554,7 +569,7 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     else bwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
 }
 
-// One token: y and the state, in place.
+// One token: y and the state, in place.  32 x 2048 takes 3 us, the time of a launch.
 template <typename X, typename G, bool ACT, bool NORM, int V>
 __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
     const int64_t nb = (p.D + 64 * V - 1) / (64 * V), n = blockIdx.x / nb;

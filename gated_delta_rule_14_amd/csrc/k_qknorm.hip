@@ -8,6 +8,11 @@
 // token, so the angle's 64-bit arithmetic is paid once for q_heads + k_heads
 // rows.  Few tokens (decode) split their heads over several waves.
 //
+// Measured (bf16): 4 x 4096 tokens of 16 + 16 heads of 128, 45 us, 6.0 TB/s
+// with part of it in the cache; 16411 tokens of 32 + 8 heads, 67 us forward
+// (5.0 TB/s, a large copy's rate) and 120 us backward (4.2 TB/s); 64 tokens of
+// 16 + 2 heads of 256, 4.8 us.
+//
 // The element that a half-split rotation pairs with sits R/16 lanes away and
 // comes by a lane shuffle; interleaved pairs are in the lane itself.
 #include <algorithm>
@@ -224,8 +229,9 @@ __device__ __forceinline__ void heads_bwd(const QkLaunch& p, const Spin<INTER>& 
     }
 }
 
-// Waves walk the tokens p.waves apart; a lane's sums for the weights stay in
-// registers until its last token, then meet over the workgroup's rows in LDS.
+// Waves walk the tokens by the grid's number of waves; a lane's sums for the
+// weights stay in registers until its last token, then meet over the
+// workgroup's rows in LDS.
 template <typename T, int LPR, bool INTER>
 __global__ __launch_bounds__(256) void qk_bwd_kernel(QkLaunch p) {
     __shared__ float2 s_cs[4][128];
