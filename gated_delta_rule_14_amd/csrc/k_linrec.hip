@@ -164,7 +164,7 @@ __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, 
             for (int k = 0; k < U; ++k) missing |= (unsigned)v[k] == ABSENT;
             if (missing) __builtin_amdgcn_s_sleep(1);
             // someone else's patience has run out: so has this thread's
-            if (missing && *polls % 1024 == 0 && __hip_atomic_load(failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+            if (missing && *polls % 1024 == 1 && __hip_atomic_load(failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
                 *polls = 1;
         } while (missing && --*polls > 0);
 #pragma unroll
