@@ -3,8 +3,10 @@
 //
 // The tile table: tiles of `tile`
 // tokens that restart at every sequence start, made on the device from the
-// caller's cu_seqlens.  Offsets are clamped into [0, T] (end >= start), so
-// invalid ones give wrong results but never an access out of bounds.
+// caller's cu_seqlens.  Offsets are clamped into [0, T] (end >= start), and a
+// sequence whose tiles do not all fit the table (which takes offsets that
+// decrease) is taken as empty, so invalid ones give wrong results but never an
+// access out of bounds or a wait for a tile that is not there.
 //
 // One workgroup: a prefix sum over the sequences' tile counts, 1024 at a
 // time, then each wave writes the rows of whole sequences, 64 at a time.
@@ -43,14 +45,17 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
             total += s_sum[w];
         }
         const int64_t first = min(before + inc - nc, a.max_tiles);
-        s_seq[tid] = make_int4((int)s, (int)len, (int)first, (int)nc);
+        if (before + inc > a.max_tiles) len = 0;
+        s_seq[tid] = make_int4((int)s, (int)len, (int)first, (int)min(nc, a.max_tiles - first));
         if (n < a.N) a.seqs[n] = make_int4((int)s, (int)len, (int)first, 0);
         __syncthreads();
         for (int i = wave; i < 1024 && base + i < a.N; i += 16) {
             const int4 q = s_seq[i];
-            for (int64_t j = lane; j < q.w && q.z + j < a.max_tiles; j += 64)
-                a.table[q.z + j] = TileRow{(int)(q.x + j * a.tile), (int)min((int64_t)a.tile, q.y - j * a.tile),
-                                           (int)(base + i), (int)j, q.w, q.y, {0, 0}};
+            for (int64_t j = lane; j < q.w; j += 64)
+                a.table[q.z + j] = q.y == 0 ? TileRow{}
+                                            : TileRow{(int)(q.x + j * a.tile),
+                                                      (int)min((int64_t)a.tile, q.y - j * a.tile), (int)(base + i),
+                                                      (int)j, q.w, q.y, {0, 0}};
         }
         carry += total;
     }
