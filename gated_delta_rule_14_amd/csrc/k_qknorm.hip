@@ -187,24 +187,30 @@ __global__ __launch_bounds__(256) void qk_fwd_kernel(QkLaunch p) {
 // dx = r (dw - x r^2/n sum x dw), and the weight's gradient sums dn x r
 template <typename T, int LPR, bool INTER>
 __device__ __forceinline__ void heads_bwd(const QkLaunch& p, const Spin<INTER>& spin, const T* x, const T* dy, T* dx,
-                                          const float* w, int64_t hs, int64_t H, int lane, bool live, float* acc) {
+                                          const float* w, int64_t hs, int64_t H, int lane, float* acc) {
     constexpr int RPW = 64 / LPR;
     const int sub = lane % LPR, e0 = 8 * sub;
     const bool in = e0 < p.D;
     const float inv_n = p.norm == GDN_NORM_RMS ? 1.f / (float)p.D : 1.f;
     float gain[8];
     gain_of(p, w, e0, in, gain);
+    // the next group's rows are loaded before this one's are worked on
+    Oct<T> nx, nd;
+    const auto fetch = [&](int64_t h) {
+        if (in && h < H) {
+            nx.load(x + h * hs + e0);
+            nd.load(dy + h * p.D + e0);
+        } else {
+            nx.zero();
+            nd.zero();
+        }
+    };
+    fetch(lane / LPR);
     for (int64_t h0 = 0; h0 < H; h0 += RPW) {
         const int64_t h = h0 + lane / LPR;
-        const bool row = in && live && h < H;
-        Oct<T> rx, rd;
-        if (row) {
-            rx.load(x + h * hs + e0);
-            rd.load(dy + h * p.D + e0);
-        } else {
-            rx.zero();
-            rd.zero();
-        }
+        const bool row = in && h < H;
+        const Oct<T> rx = nx, rd = nd;
+        if (h0 + RPW < H) fetch(h + RPW);
         float v[8], d[8], ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -229,34 +235,34 @@ __device__ __forceinline__ void heads_bwd(const QkLaunch& p, const Spin<INTER>& 
     }
 }
 
-// Waves walk the tokens by the grid's number of waves; a lane's sums for the
-// weights stay in registers until its last token, then meet over the
-// workgroup's rows in LDS.
+// Waves walk the tokens by the grid's number of waves, for q and then for k:
+// only one of the two keeps its sums for the weights in registers at a time.
+// They stay there until the lane's last token, then meet over the workgroup's rows in LDS.
 template <typename T, int LPR, bool INTER>
-__global__ __launch_bounds__(256) void qk_bwd_kernel(QkLaunch p) {
+__global__ __launch_bounds__(256, 4) void qk_bwd_kernel(QkLaunch p) {
     __shared__ float2 s_cs[4][128];
     __shared__ float s_acc[4 * (64 / LPR)][8 * LPR];
     constexpr int RPW = 64 / LPR;
     const int lane = threadIdx.x & 63, w = wave_id(), sub = lane % LPR;
-    float aq[8], ak[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-    for (int64_t token = (int64_t)blockIdx.x * 4 + w; token < p.tokens; token += (int64_t)gridDim.x * 4) {
-        Spin<INTER> spin;
-        spin_of<INTER>(p, token, s_cs[w], lane, sub, &spin);
-        heads_bwd<T, LPR, INTER>(p, spin, static_cast<const T*>(p.q) + token * p.qs,
-                                 static_cast<const T*>(p.dqo) + token * p.Hq * p.D,
-                                 static_cast<T*>(p.qo) + token * p.Hq * p.D, p.qw, p.qhs, p.Hq, lane, true, aq);
-        heads_bwd<T, LPR, INTER>(p, spin, static_cast<const T*>(p.k) + token * p.ks,
-                                 static_cast<const T*>(p.dko) + token * p.Hk * p.D,
-                                 static_cast<T*>(p.ko) + token * p.Hk * p.D, p.kw, p.khs, p.Hk, lane, true, ak);
-    }
-    if (!p.dqw && !p.dkw) return;
-#pragma unroll
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
+        const int64_t H = which ? p.Hk : p.Hq, ts = which ? p.ks : p.qs, hs = which ? p.khs : p.qhs;
+        const T* x = static_cast<const T*>(which ? p.k : p.q);
+        const T* dy = static_cast<const T*>(which ? p.dko : p.dqo);
+        T* dx = static_cast<T*>(which ? p.ko : p.qo);
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int64_t token = (int64_t)blockIdx.x * 4 + w; token < p.tokens; token += (int64_t)gridDim.x * 4) {
+            Spin<INTER> spin;
+            spin_of<INTER>(p, token, s_cs[w], lane, sub, &spin);
+            heads_bwd<T, LPR, INTER>(p, spin, x + token * ts, dy + token * H * p.D, dx + token * H * p.D,
+                                     which ? p.kw : p.qw, hs, H, lane, acc);
+        }
+        if (!(which ? p.dkw : p.dqw)) continue;
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s_acc[w * RPW + lane / LPR][8 * sub + e] = which ? ak[e] : aq[e];
+        for (int e = 0; e < 8; ++e) s_acc[w * RPW + lane / LPR][8 * sub + e] = acc[e];
         __syncthreads();
         const int e = threadIdx.x;
         if (e < p.D) {
