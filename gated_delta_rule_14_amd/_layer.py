@@ -247,7 +247,7 @@ def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_b
         workspace, have = _workspace(workspace, p.fwd, dev, x)
     _run(lib.gdn_linrec_fwd, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(), _p(h0),
          _p(cu_seqlens), y.data_ptr(), _p(ht), _p(states), _p(workspace), have)
-    _words(workspace, dev, stream, packed, p.rows > ends[0])
+    _words(workspace, dev, stream, packed, p.fwd > 0)   # (a forward workspace: tiles hand on)
     return y, ht
 
 
@@ -290,7 +290,7 @@ def linrec_bwd(x, g, dy, h0=None, dht=None, cu_seqlens=None, normalize=False, A_
         workspace, have = _workspace(workspace, p.bwd, dev, x)
     _run(lib.gdn_linrec_bwd, dev, stream, p.at, act, x.data_ptr(), g.data_ptr(), _p(h0),
          _p(cu_seqlens), dy.data_ptr(), _p(dht), _p(states), dx, dg, dh0, dA, db, _p(workspace), have)
-    _words(workspace, dev, stream, packed, p.rows > ends[0])
+    _words(workspace, dev, stream, packed, p.fwd > 0)   # (a forward workspace: tiles hand on)
     return out
 
 

@@ -46,6 +46,8 @@ struct SeqMap {
     int64_t N = 0;
     int64_t max_tiles = 0;
     int tile = 0;
+    int shorts = 0;                // > 0: tile c is sequence c where it has at most this many
+                                   // tokens, and unused where it has more (seqs != nullptr)
 };
 
 struct Tile {
@@ -60,7 +62,15 @@ struct Tile {
 // registers, for the row addresses
 __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
     Tile t;
-    if (m.table) {
+    if (m.shorts) {
+        const int4 s = m.seqs[c];
+        t.row0 = __builtin_amdgcn_readfirstlane(s.x);
+        t.len = __builtin_amdgcn_readfirstlane(s.y);
+        t.n = t.len <= m.shorts ? t.len : 0;
+        t.seq = (int)c;
+        t.j = 0;
+        t.nt = 1;
+    } else if (m.table) {
         const TileRow r = m.table[c];
         t.row0 = __builtin_amdgcn_readfirstlane(r.row0);
         t.n = __builtin_amdgcn_readfirstlane(r.n);
@@ -82,10 +92,11 @@ __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
 }
 
 // Packed offsets to the table of SeqMap; words[0] = the check of the offsets.
+// Sequences of up to `shorts` tokens get no tile (they run by SeqMap::shorts).
 struct TileTableLaunch {
     const int64_t* cu_seqlens;
     int64_t N, T, max_tiles;
-    int tile;
+    int tile, shorts;
     TileRow* table;
     int4* seqs;
     int* words;
@@ -116,9 +127,12 @@ struct LinrecLaunch {
     const float *h0 = nullptr, *dht = nullptr;
     void *y = nullptr, *dx = nullptr, *dg = nullptr;
     float *ht = nullptr, *dh0 = nullptr, *dA_log = nullptr, *ddt_bias = nullptr;
+    // Sequences of up to 16 or 64 tokens run without hand-offs: all of an unpacked call's
+    // (small: which of the two, 0: tiles of map.tile), or the packed ones among others (shorts)
+    int small = 0, shorts = 0;
     float* states = nullptr;      // [max_tiles][D] the states entering the tiles
     bool own_states = false;      // backward: states is workspace, to be filled first
-    float* part = nullptr;        // [max_tiles][2][D] sums of dA_log and ddt_bias (backward)
+    float* part = nullptr;        // [max_tiles, then N with shorts][2][D] sums of dA_log and ddt_bias (backward)
     double* sums = nullptr;       // shares of the sums of part
     // hand-offs between the tiles of a sequence; nullptr where every sequence is one tile
     uint64_t *pairs = nullptr, *groups = nullptr;   // [max_tiles][D], [max_tiles / 16 + 1][D]

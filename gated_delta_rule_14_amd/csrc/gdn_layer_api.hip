@@ -2,6 +2,8 @@
 // gdn_short_conv_*): argument checks, workspace layouts and launches.  As in
 // gdn_api.hip nothing here allocates or synchronises, and a call that returns
 // an error has launched nothing.
+#include <algorithm>
+
 #include "gdn_layer.hpp"
 
 namespace {
@@ -55,10 +57,11 @@ struct TileLayout {
     size_t seqs, table, end;
     int64_t tiles, nt;
 };
-TileLayout tile_layout(int64_t B, int64_t T, int64_t N, int tile) {
+// (sequences of up to `shorts` tokens have no tiles)
+TileLayout tile_layout(int64_t B, int64_t T, int64_t N, int tile, int shorts = 0) {
     TileLayout L;
     L.nt = (T + tile - 1) / tile;
-    L.tiles = N > 0 ? L.nt + N : B * L.nt;
+    L.tiles = N > 0 ? L.nt + std::min(N, T / (shorts + 1)) : B * L.nt;
     L.seqs = 256;
     L.table = L.seqs + align256(N > 0 ? (size_t)N * 16 : 0);
     L.end = L.table + align256(N > 0 ? (size_t)L.tiles * sizeof(gdn::TileRow) : 0);
@@ -80,13 +83,14 @@ gdn::SeqMap seq_map(const TileLayout& L, int64_t B, int64_t T, int64_t N, int ti
     return m;
 }
 
-gdn_status make_table(const gdn::SeqMap& m, const int64_t* cu, void* ws, hipStream_t st) {
+gdn_status make_table(const gdn::SeqMap& m, const int64_t* cu, void* ws, hipStream_t st, int shorts = 0) {
     gdn::TileTableLaunch t;
     t.cu_seqlens = cu;
     t.N = m.N;
     t.T = m.T;
     t.max_tiles = m.max_tiles;
     t.tile = m.tile;
+    t.shorts = shorts;
     t.table = const_cast<gdn::TileRow*>(m.table);
     t.seqs = const_cast<int4*>(m.seqs);
     t.words = static_cast<int*>(ws);
@@ -137,14 +141,26 @@ gdn_status check_linrec(const gdn_linrec_desc* d, const gdn_activation* act, gdn
 // tiles (where the caller kept none) and the tiles' parameter sums.
 struct LinrecLayout {
     TileLayout t;
+    int small, shorts;         // as in LinrecLaunch
     bool hand_offs;
     size_t pairs, groups, states, part, sums, total;
 };
 LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
     LinrecLayout L;
     const int64_t D = d->channels;
-    L.t = tile_layout(d->batch, d->seq_len, d->num_seqs, LINREC_TILE);
-    L.hand_offs = d->num_seqs > 0 || L.t.nt > 1;
+    // Sequences of up to 16 tokens run by a wave or two instead of a tile's workgroup of 8 or
+    // 16, of up to 64 by half of it (256 sequences of 4 tokens, 4096 channels: forward 124 ->
+    // 11 us, backward 339 -> 31). Of packed input only the mean length is known here: short
+    // ones are looked for where it is below half a tile (2500 sequences of 3 tokens: 1267 ->
+    // 278 and 3507 -> 444 us).
+    const bool packed = d->num_seqs > 0;
+    const int64_t T = d->seq_len, mean = packed ? T / d->num_seqs : T;
+    const int few = mean > 64 - packed ? 0 : mean > 16 - packed ? 64 : 16;
+    L.small = packed ? 0 : few;
+    L.shorts = packed ? few : 0;
+    L.t = tile_layout(d->batch, T, d->num_seqs, LINREC_TILE, L.shorts);
+    L.hand_offs = packed || L.t.nt > 1;
+    const int64_t rows = L.t.tiles + (L.shorts ? d->num_seqs : 0);
     size_t off = L.hand_offs || backward ? L.t.end : 0;
     L.pairs = off;
     if (L.hand_offs) off += align256((size_t)L.t.tiles * D * 8);
@@ -153,9 +169,9 @@ LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
     L.states = off;
     if (backward) off += align256((size_t)L.t.tiles * D * 4);
     L.part = off;
-    if (backward) off += align256((size_t)L.t.tiles * 2 * D * 4);
+    if (backward) off += align256((size_t)rows * 2 * D * 4);
     L.sums = off;
-    if (backward) off += sums_bytes(L.t.tiles, 2 * D);
+    if (backward) off += sums_bytes(rows, 2 * D);
     L.total = off;
     return L;
 }
@@ -164,6 +180,7 @@ LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
 gdn_status check_linrec_grid(const gdn_linrec_desc* d, const LinrecLayout& L) {
     const double D = (double)d->channels, N = (double)(d->num_seqs > 0 ? d->num_seqs : d->batch);
     gdn_status s = check_grid((double)L.t.tiles * ((D + 63) / 64), 1024);
+    if (s == GDN_OK && L.shorts) s = check_grid(N * ((D + 63) / 64), 512);
     if (s == GDN_OK) s = check_grid((N + (double)L.t.tiles) * ((D + 511) / 512), 256);
     return s != GDN_OK ? s : check_grid(2 * ((D + 15) / 16), 1024);
 }
@@ -172,6 +189,8 @@ void linrec_place(gdn::LinrecLaunch* a, const gdn_linrec_desc* d, const LinrecLa
     char* ws = static_cast<char*>(workspace);
     a->map = seq_map(L.t, d->batch, d->seq_len, d->num_seqs, LINREC_TILE, workspace);
     a->words = reinterpret_cast<int*>(ws);
+    a->small = L.small;
+    a->shorts = L.shorts;
     if (L.hand_offs) {
         a->pairs = reinterpret_cast<uint64_t*>(ws + L.pairs);
         a->groups = reinterpret_cast<uint64_t*>(ws + L.groups);
@@ -357,7 +376,7 @@ gdn_status gdn_linrec_fwd(const gdn_linrec_desc* d, const gdn_activation* act_in
     a.y = y;
     a.ht = ht;
     a.states = states;
-    if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream)) != GDN_OK) return s;
+    if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream, L.shorts)) != GDN_OK) return s;
     hipError_t e = gdn::launch_linrec_fwd(a);
     return e == hipSuccess ? api_ok() : hip_fail(e, "linear recurrence launch");
 }
@@ -396,7 +415,7 @@ gdn_status gdn_linrec_bwd(const gdn_linrec_desc* d, const gdn_activation* act_in
     a.states = states ? const_cast<float*>(states) : reinterpret_cast<float*>(ws + L.states);
     a.part = reinterpret_cast<float*>(ws + L.part);
     a.sums = reinterpret_cast<double*>(ws + L.sums);
-    if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream)) != GDN_OK) return s;
+    if (cu_seqlens && (s = make_table(a.map, cu_seqlens, workspace, a.stream, L.shorts)) != GDN_OK) return s;
     hipError_t e = gdn::launch_linrec_bwd(a);
     return e == hipSuccess ? api_ok() : hip_fail(e, "linear recurrence backward launch");
 }

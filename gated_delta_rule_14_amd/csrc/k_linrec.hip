@@ -282,13 +282,18 @@ __device__ __forceinline__ Spot spot_of(const LinrecLaunch& p, const Tile& t, in
     s.c = min(c0 + s.lane * V, p.D - V);
     return s;
 }
-// rows of the wave's tokens; of a tile that is not FULL the last one again past its end
+// A tile that is not FULL is worked on four tokens at a time: those past its end
+// repeat its last row and count as a = 1, u = 0, groups that are wholly past it are left
+// out (a condition to every token would leave nothing to overlap).
+constexpr int QUAD = 4;
+// row of the wave's token i
 template <bool FULL, typename T>
 __device__ __forceinline__ const T* row_at(const T* tile, int64_t stride, const Spot& s, const Tile& t, int i) {
     return in_scalar(tile + (int64_t)(FULL ? s.first + i : min(s.first + i, t.n - 1)) * stride);
 }
 
-template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+// HAND: tiles of a sequence hand their pairs on; without it every sequence is one tile.
+template <bool FULL, bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_pA)[64 * V],
                                          float (*s_pH)[64 * V]) {
@@ -300,9 +305,13 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
     Raw<X, V> rx[S];
     Raw<G, V> rg[S];
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        rg[i].load(row_at<FULL>(g, p.gs, s, t, i), og);
-        rx[i].load(row_at<FULL>(x, p.xs, s, t, i), ox);
+    for (int q = 0; q < S; q += QUAD) {
+        if (!FULL && q >= s.nv) continue;     // the same for the whole wave, here and below
+#pragma unroll
+        for (int i = q; i < q + QUAD; ++i) {
+            rg[i].load(row_at<FULL>(g, p.gs, s, t, i), og);
+            rx[i].load(row_at<FULL>(x, p.xs, s, t, i), ox);
+        }
     }
     float rate2[V], bias[V], A[V], H[V], a[S][V], u[S][V];
 #pragma unroll
@@ -313,15 +322,18 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
         H[e] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
+    for (int q = 0; q < S; q += QUAD) {
+        if (!FULL && q >= s.nv) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const Gate q = gate_of<ACT, NORM, false>(rg[i].get(e), rate2[e], bias[e]);
-            a[i][e] = FULL || i < s.nv ? q.a : 1.f;
-            u[i][e] = FULL || i < s.nv ? q.m * rx[i].get(e) : 0.f;
-            H[e] = a[i][e] * H[e] + u[i][e];
-            A[e] *= a[i][e];
-        }
+        for (int i = q; i < q + QUAD; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const Gate w = gate_of<ACT, NORM, false>(rg[i].get(e), rate2[e], bias[e]);
+                a[i][e] = FULL || i < s.nv ? w.a : 1.f;
+                u[i][e] = FULL || i < s.nv ? w.m * rx[i].get(e) : 0.f;
+                H[e] = a[i][e] * H[e] + u[i][e];
+                A[e] *= a[i][e];
+            }
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -330,62 +342,73 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
     }
     __syncthreads();
     const int tid = threadIdx.x;
-    const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
-    const bool own = part == 0 && c0 + k < p.D;
-    float tA = 1.f, tH = 0.f;
-    const bool live = part < NT && c0 + k < p.D, closes = closes_group(t.j, t.nt);
-    if (own) {
-#pragma unroll 4
-        for (int i = 0; i < NW; ++i) {
-            tH = s_A[i][k] * tH + s_H[i][k];
-            tA *= s_A[i][k];
-        }
-    }
-    if (live && part < 2) {
-        const float start = t.j == 0 && part == 0 && p.h0 ? p.h0[t.seq * p.D + c0 + k] : 0.f;
-        if (part == 0) publish_tile(p, tile, t.j, t.nt, c0 + k, tA, tH, start);
-        enter_own(p, tile, t.j, 1, c0 + k, part, start, &s_pA[part][k], &s_pH[part][k]);
-    }
-    if (closes) {        // before waiting for other groups, or the groups would wait in a row
-        __syncthreads();
-        if (own) publish_group<CB>(p, tile, t.j, c0 + k, tA, tH, s_pA, s_pH, k);
-    }
-    if (live && part >= 2) enter_groups(p, tile, t.j, 1, c0 + k, part, &s_pA[part][k], &s_pH[part][k]);
-    __syncthreads();
-    if (own) {
-        const float in = entering<CB>(s_pA, s_pH, k);
-        if (p.states) p.states[tile * p.D + c0 + k] = in;
-        if (p.ht && t.j + 1 == t.nt) p.ht[t.seq * p.D + c0 + k] = tA * in + tH;
-    }
-    if (!p.y) return;
     float h[V];
+    if constexpr (HAND) {
+        const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
+        const bool own = part == 0 && c0 + k < p.D;
+        float tA = 1.f, tH = 0.f;
+        const bool live = part < NT && c0 + k < p.D, closes = closes_group(t.j, t.nt);
+        if (own) {
+#pragma unroll 4
+            for (int i = 0; i < NW; ++i) {
+                tH = s_A[i][k] * tH + s_H[i][k];
+                tA *= s_A[i][k];
+            }
+        }
+        if (live && part < 2) {
+            const float start = t.j == 0 && part == 0 && p.h0 ? p.h0[t.seq * p.D + c0 + k] : 0.f;
+            if (part == 0) publish_tile(p, tile, t.j, t.nt, c0 + k, tA, tH, start);
+            enter_own(p, tile, t.j, 1, c0 + k, part, start, &s_pA[part][k], &s_pH[part][k]);
+        }
+        if (closes) {        // before waiting for other groups, or the groups would wait in a row
+            __syncthreads();
+            if (own) publish_group<CB>(p, tile, t.j, c0 + k, tA, tH, s_pA, s_pH, k);
+        }
+        if (live && part >= 2) enter_groups(p, tile, t.j, 1, c0 + k, part, &s_pA[part][k], &s_pH[part][k]);
+        __syncthreads();
+        if (own) {
+            const float in = entering<CB>(s_pA, s_pH, k);
+            if (p.states) p.states[tile * p.D + c0 + k] = in;
+            if (p.ht && t.j + 1 == t.nt) p.ht[t.seq * p.D + c0 + k] = tA * in + tH;
+        }
+        if (!p.y) return;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        h[e] = entering<CB>(s_pA, s_pH, s.lane * V + e);
-        for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
+        for (int e = 0; e < V; ++e) h[e] = entering<CB>(s_pA, s_pH, s.lane * V + e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = p.h0 ? p.h0[t.seq * p.D + s.c + e] : 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
     if (!s.in) return;
     X* y = static_cast<X*>(p.y) + (t.row0 + s.first) * p.ys;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
+        if (!FULL && i >= s.nv) continue;
 #pragma unroll
         for (int e = 0; e < V; ++e) h[e] = a[i][e] * h[e] + u[i][e];
-        if (FULL || i < s.nv) Raw<X, V>::store(in_scalar(y + i * p.ys), ox, h);
+        if (p.y) Raw<X, V>::store(in_scalar(y + i * p.ys), ox, h);
+    }
+    // the wave of the sequence's last token
+    if (!HAND && p.ht && s.nv > 0 && s.first + s.nv == t.n) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) p.ht[t.seq * p.D + s.c + e] = h[e];
     }
 }
 
-template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
-    static_assert(NT * CB <= 64 * NW, "NT threads to a channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[NT][CB], s_pH[NT][CB];
+    static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[HAND ? NT : 1][CB], s_pH[HAND ? NT : 1][CB];
     __shared__ unsigned s_ticket;
-    const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB), tile = k / nb;
+    const unsigned k = HAND ? ticket_of(p, &s_ticket) : blockIdx.x, nb = (unsigned)((p.D + CB - 1) / CB), tile = k / nb;
     const int64_t c0 = (int64_t)(k - tile * nb) * CB;
     const Tile t = tile_of(p.map, tile);
     if (t.n <= 0) return;
-    if (t.n == S * NW) fwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
-    else fwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
+    if (t.n == S * NW) fwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
+    else fwd_tile<false, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
 }
 
 // The same tiles taken from the last token: e = a (dy + e') is what a token
@@ -396,7 +419,7 @@ __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) 
 // channels, bf16, raw gates, normalised: 116 us against 66 us of bytes and 73
 // us of ALU slots; one workgroup fills a CU, so the loads and the hand-off of
 // a tile are not hidden by another.
-template <bool FULL, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <bool FULL, bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_E)[64 * V],
                                          float (*s_pA)[64 * V], float (*s_pE)[64 * V], float* s_in,
@@ -414,10 +437,14 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
     {
         Raw<G, V> rg[S];
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            rg[i].load(row_at<FULL>(g, p.gs, s, t, i), og);
-            rx[i].load(row_at<FULL>(x, p.xs, s, t, i), ox);
-            rd[i].load(row_at<FULL>(dy, p.ys, s, t, i), ox);
+        for (int q = 0; q < S; q += QUAD) {
+            if (!FULL && q >= s.nv) continue;
+#pragma unroll
+            for (int i = q; i < q + QUAD; ++i) {
+                rg[i].load(row_at<FULL>(g, p.gs, s, t, i), og);
+                rx[i].load(row_at<FULL>(x, p.xs, s, t, i), ox);
+                rd[i].load(row_at<FULL>(dy, p.ys, s, t, i), ox);
+            }
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -428,23 +455,30 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
             E[e] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
+        for (int q = 0; q < S; q += QUAD) {
+            if (!FULL && q >= s.nv) continue;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const Gate q = gate_of<ACT, NORM, true>(rg[i].get(e), rate2[e], bias[e]);
-                a[i][e] = FULL || i < s.nv ? q.a : 1.f;
-                m[i][e] = q.m;
-                if (ACT) s_gate[i * V + e][tid] = f32x2v{q.l2, q.sg};
-                H[e] = a[i][e] * H[e] + (FULL || i < s.nv ? q.m * rx[i].get(e) : 0.f);
-                A[e] *= a[i][e];
+            for (int i = q; i < q + QUAD; ++i) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const Gate w = gate_of<ACT, NORM, true>(rg[i].get(e), rate2[e], bias[e]);
+                    a[i][e] = FULL || i < s.nv ? w.a : 1.f;
+                    m[i][e] = w.m;
+                    if (ACT) s_gate[i * V + e][tid] = f32x2v{w.l2, w.sg};
+                    H[e] = a[i][e] * H[e] + (FULL || i < s.nv ? w.m * rx[i].get(e) : 0.f);
+                    A[e] *= a[i][e];
+                }
+                // a token at a time where registers, not overlap, are short
+                if (HAND) __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);   // a token at a time: registers, not overlap, are short
         }
     }
 #pragma unroll
-    for (int i = S - 1; i >= 0; --i)
+    for (int i = S - 1; i >= 0; --i) {
+        if (!FULL && i >= s.nv) continue;
 #pragma unroll
-        for (int e = 0; e < V; ++e) E[e] = a[i][e] * ((FULL || i < s.nv ? rd[i].get(e) : 0.f) + E[e]);
+        for (int e = 0; e < V; ++e) E[e] = a[i][e] * (rd[i].get(e) + E[e]);
+    }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         s_A[s.w][s.lane * V + e] = A[e];
@@ -452,50 +486,63 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
         s_E[s.w][s.lane * V + e] = E[e];
     }
     __syncthreads();
-    const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
-    const bool own = part == 0 && c0 + k < p.D;
-    const int back = t.nt - 1 - t.j;                           // the tile counted from the sequence's end
-    float tA = 1.f, tE = 0.f;
-    const bool live = part < NT && c0 + k < p.D, closes = closes_group(back, t.nt);
-    if (own) {
-#pragma unroll 2
-        for (int i = NW - 1; i >= 0; --i) {
-            tE = s_A[i][k] * tE + s_E[i][k];
-            tA *= s_A[i][k];
-        }
-        s_in[k] = p.states[tile * p.D + c0 + k];
-    }
-    if (live && part < 2) {
-        const float start = back == 0 && part == 0 && p.dht ? p.dht[t.seq * p.D + c0 + k] : 0.f;
-        if (part == 0) publish_tile(p, tile, back, t.nt, c0 + k, tA, tE, start);
-        enter_own(p, tile, back, -1, c0 + k, part, start, &s_pA[part][k], &s_pE[part][k]);
-    }
-    if (closes) {        // before waiting for other groups, or the groups would wait in a row
-        __syncthreads();
-        if (own) publish_group<CB>(p, tile, back, c0 + k, tA, tE, s_pA, s_pE, k);
-    }
-    if (live && part >= 2) enter_groups(p, tile, back, -1, c0 + k, part, &s_pA[part][k], &s_pE[part][k]);
-    __syncthreads();
-    if (own) {
-        if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + c0 + k] = tA * entering<CB>(s_pA, s_pE, k) + tE;
-    }
     float h[V], d[V], sA[V], sb[V], before[S][V];
+    if constexpr (HAND) {
+        const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
+        const bool own = part == 0 && c0 + k < p.D;
+        const int back = t.nt - 1 - t.j;                           // the tile counted from the sequence's end
+        float tA = 1.f, tE = 0.f;
+        const bool live = part < NT && c0 + k < p.D, closes = closes_group(back, t.nt);
+        if (own) {
+#pragma unroll 2
+            for (int i = NW - 1; i >= 0; --i) {
+                tE = s_A[i][k] * tE + s_E[i][k];
+                tA *= s_A[i][k];
+            }
+            s_in[k] = p.states[tile * p.D + c0 + k];
+        }
+        if (live && part < 2) {
+            const float start = back == 0 && part == 0 && p.dht ? p.dht[t.seq * p.D + c0 + k] : 0.f;
+            if (part == 0) publish_tile(p, tile, back, t.nt, c0 + k, tA, tE, start);
+            enter_own(p, tile, back, -1, c0 + k, part, start, &s_pA[part][k], &s_pE[part][k]);
+        }
+        if (closes) {        // before waiting for other groups, or the groups would wait in a row
+            __syncthreads();
+            if (own) publish_group<CB>(p, tile, back, c0 + k, tA, tE, s_pA, s_pE, k);
+        }
+        if (live && part >= 2) enter_groups(p, tile, back, -1, c0 + k, part, &s_pA[part][k], &s_pE[part][k]);
+        __syncthreads();
+        if (own) {
+            if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + c0 + k] = tA * entering<CB>(s_pA, s_pE, k) + tE;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            h[e] = s_in[s.lane * V + e];
+            d[e] = entering<CB>(s_pA, s_pE, s.lane * V + e);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            h[e] = p.h0 ? p.h0[t.seq * p.D + s.c + e] : 0.f;
+            d[e] = p.dht ? p.dht[t.seq * p.D + s.c + e] : 0.f;
+        }
+    }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        h[e] = s_in[s.lane * V + e];
-        d[e] = entering<CB>(s_pA, s_pE, s.lane * V + e);
         for (int i = 0; i < s.w; ++i) h[e] = s_A[i][s.lane * V + e] * h[e] + s_H[i][s.lane * V + e];
         for (int i = NW - 1; i > s.w; --i) d[e] = s_A[i][s.lane * V + e] * d[e] + s_E[i][s.lane * V + e];
         sA[e] = 0.f;
         sb[e] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < S; ++i)
+    for (int i = 0; i < S; ++i) {
+        if (!FULL && i >= s.nv) continue;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             before[i][e] = h[e];
             h[e] = a[i][e] * h[e] + m[i][e] * rx[i].get(e);
         }
+    }
     X* dx = static_cast<X*>(p.dx) + (t.row0 + s.first) * p.D;
     G* dg = static_cast<G*>(p.dg) + (t.row0 + s.first) * p.D;
 #pragma unroll
@@ -524,6 +571,10 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
         }
         __builtin_amdgcn_sched_barrier(0);
     }
+    if (!HAND && p.dh0 && s.w == 0 && s.in) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) p.dh0[t.seq * p.D + s.c + e] = d[e];
+    }
     if (!ACT) return;
     __syncthreads();                                          // the waves have read the pairs
 #pragma unroll
@@ -532,41 +583,42 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
         s_H[s.w][s.lane * V + e] = sb[e];
     }
     __syncthreads();
-    if (tid < CB && c0 + tid < p.D) {
+    for (int k = tid; k < CB && c0 + k < p.D; k += 64 * NW) {
         float tA = 0.f, tb = 0.f;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            tA += s_A[i][tid];
-            tb += s_H[i][tid];
+            tA += s_A[i][k];
+            tb += s_H[i][k];
         }
-        p.part[2 * tile * p.D + c0 + tid] = LN2 * tA;
-        p.part[(2 * tile + 1) * p.D + c0 + tid] = tb;
+        p.part[2 * tile * p.D + c0 + k] = LN2 * tA;
+        p.part[(2 * tile + 1) * p.D + c0 + k] = tb;
     }
 }
 
-template <typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
-    static_assert(NT * CB <= 64 * NW, "NT threads to a channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB], s_pA[NT][CB], s_pE[NT][CB], s_in[CB];
+    static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB];
+    __shared__ float s_pA[HAND ? NT : 1][CB], s_pE[HAND ? NT : 1][CB], s_in[CB];
     // log2 a and sigmoid of every token, each thread's own: they are wanted again only at
     // the end, and next to a, m, x and dy there are no registers for them
     __shared__ f32x2v s_gate[ACT ? S * V : 1][64 * NW];
     __shared__ unsigned s_ticket;
-    const unsigned k = ticket_of(p, &s_ticket), nb = (unsigned)((p.D + CB - 1) / CB);
-    const unsigned tile = (unsigned)p.map.max_tiles - 1 - k / nb;
+    const unsigned k = HAND ? ticket_of(p, &s_ticket) : blockIdx.x, nb = (unsigned)((p.D + CB - 1) / CB);
+    const unsigned tile = HAND ? (unsigned)p.map.max_tiles - 1 - k / nb : k / nb;
     const int64_t c0 = (int64_t)(k % nb) * CB;
     const Tile t = tile_of(p.map, tile);
-    const int tid = threadIdx.x;
     if (t.n <= 0) {
-        if (ACT && tid < CB && c0 + tid < p.D) {
-            p.part[(int64_t)(2 * tile) * p.D + c0 + tid] = 0.f;
-            p.part[(int64_t)(2 * tile + 1) * p.D + c0 + tid] = 0.f;
-        }
+        if (ACT)
+            for (int i = threadIdx.x; i < CB && c0 + i < p.D; i += 64 * NW) {
+                p.part[(int64_t)(2 * tile) * p.D + c0 + i] = 0.f;
+                p.part[(int64_t)(2 * tile + 1) * p.D + c0 + i] = 0.f;
+            }
         return;
     }
-    if (t.n == S * NW) bwd_tile<true, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
-    else bwd_tile<false, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
+    if (t.n == S * NW) bwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
+    else bwd_tile<false, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
 }
 
 // One token: y and the state, in place.  32 x 2048 takes 3 us, the time of a launch.
@@ -594,20 +646,29 @@ __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
 }
 
 // ---- launches
-enum { FWD, BWD, STEP };
+enum { FWD, FWD16, FWD64, BWD, BWD16, BWD64, STEP };
+template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+static void fwd(const LinrecLaunch& p, int64_t blocks) {
+    hipLaunchKernelGGL((linrec_fwd_kernel<HAND, X, G, ACT, NORM, V, S, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0,
+                       p.stream, p);
+}
+template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+static void bwd(const LinrecLaunch& p, int64_t blocks) {
+    hipLaunchKernelGGL((linrec_bwd_kernel<HAND, X, G, ACT, NORM, V, S, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0,
+                       p.stream, p);
+}
 template <int WHICH, typename X, typename G, bool ACT, bool NORM, int V>
 static hipError_t go2(const LinrecLaunch& p) {
-    const int64_t nb = (p.D + 64 * V - 1) / (64 * V);
-    if constexpr (WHICH == FWD) {
-        hipLaunchKernelGGL((linrec_fwd_kernel<X, G, ACT, NORM, V, 16, 8>), dim3((unsigned)(nb * p.map.max_tiles)),
-                           dim3(512), 0, p.stream, p);
-    } else if constexpr (WHICH == BWD) {
-        hipLaunchKernelGGL((linrec_bwd_kernel<X, G, ACT, NORM, V, 8, 16>), dim3((unsigned)(nb * p.map.max_tiles)),
-                           dim3(1024), 0, p.stream, p);
-    } else {
+    const int64_t nb = (p.D + 64 * V - 1) / (64 * V), tiles = nb * (p.map.shorts ? p.map.N : p.map.max_tiles);
+    if constexpr (WHICH == FWD) fwd<true, X, G, ACT, NORM, V, 16, 8>(p, tiles);
+    else if constexpr (WHICH == FWD16) fwd<false, X, G, ACT, NORM, V, 16, 1>(p, tiles);
+    else if constexpr (WHICH == FWD64) fwd<false, X, G, ACT, NORM, V, 16, 4>(p, tiles);
+    else if constexpr (WHICH == BWD) bwd<true, X, G, ACT, NORM, V, 8, 16>(p, tiles);
+    else if constexpr (WHICH == BWD16) bwd<false, X, G, ACT, NORM, V, 8, 2>(p, tiles);
+    else if constexpr (WHICH == BWD64) bwd<false, X, G, ACT, NORM, V, 8, 8>(p, tiles);
+    else
         hipLaunchKernelGGL((linrec_step_kernel<X, G, ACT, NORM, V>), dim3((unsigned)(nb * p.map.N)), dim3(64), 0,
                            p.stream, p);
-    }
     return hipGetLastError();
 }
 template <int WHICH, typename X, typename G, int V>
@@ -643,24 +704,42 @@ static hipError_t clear(const LinrecLaunch& p, const float* from, float* to) {
     return hipGetLastError();
 }
 
+// the packed sequences of up to p.shorts tokens
+static LinrecLaunch short_ones(const LinrecLaunch& p) {
+    LinrecLaunch q = p;
+    q.map.shorts = p.shorts;
+    q.states = nullptr;
+    if (q.part) q.part += 2 * p.map.max_tiles * p.D;
+    return q;
+}
+static hipError_t fwd_few(const LinrecLaunch& p, int few) { return few == 16 ? go<FWD16>(p) : go<FWD64>(p); }
+static hipError_t bwd_few(const LinrecLaunch& p, int few) { return few == 16 ? go<BWD16>(p) : go<BWD64>(p); }
+
 hipError_t launch_linrec_fwd(const LinrecLaunch& p) {
     hipError_t e = clear(p, p.h0, p.ht);
-    if (e != hipSuccess || p.map.max_tiles == 0) return e;
+    if (e != hipSuccess || p.map.T == 0) return e;
+    if (p.small) return fwd_few(p, p.small);
+    if (p.shorts && (p.y || p.ht) && (e = fwd_few(short_ones(p), p.shorts)) != hipSuccess) return e;
     return go<FWD>(p);
 }
 
 hipError_t launch_linrec_bwd(const LinrecLaunch& p) {
     hipError_t e;
-    if (p.own_states && p.map.max_tiles > 0) {   // the states entering the tiles were not kept
+    if (p.own_states && !p.small && p.map.T > 0) {   // the states entering the tiles were not kept
         LinrecLaunch f = p;
         f.y = nullptr;
         f.ht = nullptr;
         if ((e = launch_linrec_fwd(f)) != hipSuccess) return e;
     }
     if ((e = clear(p, p.dht, p.dh0)) != hipSuccess) return e;
-    if (p.map.max_tiles > 0 && (e = go<BWD>(p)) != hipSuccess) return e;
+    if (p.map.T > 0) {
+        if (p.small) e = bwd_few(p, p.small);
+        else if (!p.shorts || (e = bwd_few(short_ones(p), p.shorts)) == hipSuccess) e = go<BWD>(p);
+        if (e != hipSuccess) return e;
+    }
     if (!(p.act.flags & ACT_GATE)) return hipSuccess;
-    return launch_row_sum(RowSumLaunch{p.part, p.map.max_tiles, p.D, 1, 2, p.dA_log, p.ddt_bias, p.sums, p.stream});
+    const int64_t rows = p.map.T > 0 ? p.map.max_tiles + (p.shorts ? p.map.N : 0) : 0;
+    return launch_row_sum(RowSumLaunch{p.part, rows, p.D, 1, 2, p.dA_log, p.ddt_bias, p.sums, p.stream});
 }
 
 hipError_t launch_linrec_step(const LinrecLaunch& p) { return go<STEP>(p); }

@@ -30,7 +30,7 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
             if (re < rs || (n == 0 && rs != 0) || (n == a.N - 1 && re != a.T)) atomicOr(&s_bad, 1);
             s = min(max(rs, (int64_t)0), a.T);
             len = min(max(re, s), a.T) - s;
-            nc = (len + a.tile - 1) / a.tile;
+            nc = len <= a.shorts ? 0 : (len + a.tile - 1) / a.tile;
         }
         int64_t inc = nc;                               // inclusive scan over the wave
         for (int off = 1; off < 64; off <<= 1) {
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
             total += s_sum[w];
         }
         const int64_t first = min(before + inc - nc, a.max_tiles);
-        if (before + inc > a.max_tiles) len = 0;
+        if (nc > 0 && before + inc > a.max_tiles) len = 0;
         s_seq[tid] = make_int4((int)s, (int)len, (int)first, (int)min(nc, a.max_tiles - first));
         if (n < a.N) a.seqs[n] = make_int4((int)s, (int)len, (int)first, 0);
         __syncthreads();

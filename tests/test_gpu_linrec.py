@@ -78,6 +78,24 @@ def test_many_short_sequences(gpu_lib):
     both(gpu_lib, inputs(12, 1, int(cu[-1]), 8, N=2500), cu)
 
 
+@pytest.mark.parametrize("D", [8, 129, 200])
+def test_short_among_long_sequences(gpu_lib, D):
+    """Packed input whose mean length is short: sequences on either side of 16 and of 64 tokens."""
+    for more in (0, 50):
+        short_among_long(gpu_lib, D, (1, 2, 15, 16, 17, 18, 0, 63, 64, 65, 200, 16, 0, 300, 3, 16, 17, 128, 1, 1)
+                         + (3,) * more)
+
+
+def short_among_long(gpu_lib, D, lengths):
+    T, N = sum(lengths), len(lengths)
+    cu = torch.tensor([sum(lengths[:i]) for i in range(N + 1)])
+    print("case: linrec short among long", T, N, D, flush=True)
+    d = inputs(25, 1, T, D, BF, BF, True, N=N)
+    both(gpu_lib, d, cu, normalize=True)
+    both(gpu_lib, d, cu, h0=False, dht=False, keep=False)
+    both(gpu_lib, inputs(26, 1, T, D, F32, F32, N=N), cu)
+
+
 def test_long_sequence(gpu_lib):
     """More tiles than one group of the look-back."""
     print("case: linrec long", flush=True)
