@@ -91,7 +91,8 @@ __device__ __forceinline__ Tile tile_of(const SeqMap& m, int64_t c) {
     return t;
 }
 
-// Packed offsets to the table of SeqMap; words[0] = the check of the offsets.
+// Packed offsets to the table of SeqMap; words[0] = the check of the offsets,
+// words[2] = the rows in use (the others are at the end).
 // Sequences of up to `shorts` tokens get no tile (they run by SeqMap::shorts).
 struct TileTableLaunch {
     const int64_t* cu_seqlens;
@@ -119,6 +120,7 @@ struct RowSumLaunch {
 int64_t row_sum_shares(int64_t rows, int64_t cols);
 hipError_t launch_row_sum(const RowSumLaunch& a);
 
+constexpr int TICKET = 32;        // word of the ticket counter, a cache line away from the others
 struct LinrecLaunch {
     SeqMap map;
     Act act;                      // ACT_GATE: A_log, dt_bias [D]
@@ -136,7 +138,7 @@ struct LinrecLaunch {
     double* sums = nullptr;       // shares of the sums of part
     // hand-offs between the tiles of a sequence; nullptr where every sequence is one tile
     uint64_t *pairs = nullptr, *groups = nullptr;   // [max_tiles][D], [max_tiles / 16 + 1][D]
-    int* words = nullptr;         // check of the offsets, failed waits, ticket
+    int* words = nullptr;         // check of the offsets, failed waits, table rows in use; [TICKET]
     int64_t D = 0, xs = 0, gs = 0, ys = 0;   // channels; token strides of x, g, y / dy
     bool x_bf16 = false, g_bf16 = false;
     hipStream_t stream = nullptr;

@@ -20,7 +20,9 @@
 // never published, set by a kernel in front.
 //
 // Workgroups take their tile from a ticket counter, tiles in the order they
-// wait for each other: every tile that one waits for belongs to a workgroup
+// wait for each other, the channel blocks of a tile one after the other (a
+// counter to each block lets them drift apart: 674 -> 752 us on the packed
+// input): every tile that one waits for belongs to a workgroup
 // that is already running and that publishes without a wait (a group's pair:
 // after waits of that kind), so every wait ends.  Each is bounded all the
 // same and reports in words[1], which ends the others' waits too.
@@ -239,7 +241,7 @@ __global__ __launch_bounds__(256) void linrec_clear_kernel(LinrecLaunch p, const
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.pairs) {
         if (!p.map.table) p.words[0] = 0;
         p.words[1] = 0;
-        p.words[2] = 0;
+        p.words[TICKET] = 0;
     }
     const int64_t tiles = p.pairs ? p.map.max_tiles : 0;
     if (i >= tiles) {
@@ -256,12 +258,25 @@ __global__ __launch_bounds__(256) void linrec_clear_kernel(LinrecLaunch p, const
     }
 }
 
-// tile and channel block of this workgroup: by ticket where tiles wait for each other
-__device__ __forceinline__ unsigned ticket_of(const LinrecLaunch& p, unsigned* s) {
-    if (!p.pairs) return blockIdx.x;
-    if (threadIdx.x == 0) *s = atomicAdd(reinterpret_cast<unsigned*>(p.words) + 2, 1u);
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*s);
+// Tile and channel block of this workgroup (of nb blocks): by ticket where tiles
+// wait for each other.  With sequences that run without hand-offs most rows of
+// the table may be unused, and those, its last, need no ticket (one counter
+// serves 87 million a second); else the word that says so is not waited for.
+template <bool HAND>
+__device__ __forceinline__ unsigned tile_by_ticket(const LinrecLaunch& p, unsigned nb, bool backward, unsigned* block,
+                                                   unsigned* s) {
+    unsigned k = blockIdx.x, used = (unsigned)p.map.max_tiles;
+    if (HAND && p.pairs) {                 // else every sequence is one tile: no words
+        if (p.shorts) used = __builtin_amdgcn_readfirstlane((unsigned)p.words[2]);
+        if (k < used * nb) {
+            if (threadIdx.x == 0) *s = atomicAdd(reinterpret_cast<unsigned*>(p.words) + TICKET, 1u);
+            __syncthreads();
+            k = __builtin_amdgcn_readfirstlane(*s);
+        }
+    }
+    const unsigned i = k / nb;
+    *block = k - i * nb;
+    return HAND && backward && i < used ? used - 1 - i : i;
 }
 
 // A wave's place in its tile.
@@ -403,8 +418,9 @@ __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) 
     static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
     __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[HAND ? NT : 1][CB], s_pH[HAND ? NT : 1][CB];
     __shared__ unsigned s_ticket;
-    const unsigned k = HAND ? ticket_of(p, &s_ticket) : blockIdx.x, nb = (unsigned)((p.D + CB - 1) / CB), tile = k / nb;
-    const int64_t c0 = (int64_t)(k - tile * nb) * CB;
+    unsigned block;
+    const unsigned tile = tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), false, &block, &s_ticket);
+    const int64_t c0 = (int64_t)block * CB;
     const Tile t = tile_of(p.map, tile);
     if (t.n <= 0) return;
     if (t.n == S * NW) fwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
@@ -605,15 +621,15 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     // the end, and next to a, m, x and dy there are no registers for them
     __shared__ f32x2v s_gate[ACT ? S * V : 1][64 * NW];
     __shared__ unsigned s_ticket;
-    const unsigned k = HAND ? ticket_of(p, &s_ticket) : blockIdx.x, nb = (unsigned)((p.D + CB - 1) / CB);
-    const unsigned tile = HAND ? (unsigned)p.map.max_tiles - 1 - k / nb : k / nb;
-    const int64_t c0 = (int64_t)(k % nb) * CB;
+    unsigned block;
+    const unsigned tile = tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), true, &block, &s_ticket);
+    const int64_t c0 = (int64_t)block * CB;
     const Tile t = tile_of(p.map, tile);
     if (t.n <= 0) {
         if (ACT)
-            for (int i = threadIdx.x; i < CB && c0 + i < p.D; i += 64 * NW) {
-                p.part[(int64_t)(2 * tile) * p.D + c0 + i] = 0.f;
-                p.part[(int64_t)(2 * tile + 1) * p.D + c0 + i] = 0.f;
+            for (int k = threadIdx.x; k < CB && c0 + k < p.D; k += 64 * NW) {
+                p.part[(int64_t)(2 * tile) * p.D + c0 + k] = 0.f;
+                p.part[(int64_t)(2 * tile + 1) * p.D + c0 + k] = 0.f;
             }
         return;
     }

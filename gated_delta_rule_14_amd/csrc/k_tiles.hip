@@ -8,11 +8,19 @@
 // decrease) is taken as empty, so invalid ones give wrong results but never an
 // access out of bounds or a wait for a tile that is not there.
 //
-// One workgroup: a prefix sum over the sequences' tile counts, 1024 at a
-// time, then each wave writes the rows of whole sequences, 64 at a time.
+// One workgroup: a prefix sum over the sequences' tile counts, 1024 at a time;
+// each thread writes its sequence's first row, then each wave the other rows
+// of whole sequences, 64 at a time.  5 us for a few sequences.
 #include "gdn_layer.hpp"
 
 namespace gdn {
+
+// row j of sequence n: q = (first token, length, first row, rows)
+__device__ __forceinline__ void put(const TileTableLaunch& a, const int4& q, int64_t n, int64_t j) {
+    a.table[q.z + j] = q.y == 0 ? TileRow{}
+                                : TileRow{(int)(q.x + j * a.tile), (int)min((int64_t)a.tile, q.y - j * a.tile), (int)n,
+                                          (int)j, q.w, q.y, {0, 0}};
+}
 
 __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
     __shared__ int64_t s_sum[16];
@@ -49,13 +57,11 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
         s_seq[tid] = make_int4((int)s, (int)len, (int)first, (int)min(nc, a.max_tiles - first));
         if (n < a.N) a.seqs[n] = make_int4((int)s, (int)len, (int)first, 0);
         __syncthreads();
+        if (n < a.N && s_seq[tid].w > 0) put(a, s_seq[tid], n, 0);
         for (int i = wave; i < 1024 && base + i < a.N; i += 16) {
             const int4 q = s_seq[i];
-            for (int64_t j = lane; j < q.w; j += 64)
-                a.table[q.z + j] = q.y == 0 ? TileRow{}
-                                            : TileRow{(int)(q.x + j * a.tile),
-                                                      (int)min((int64_t)a.tile, q.y - j * a.tile), (int)(base + i),
-                                                      (int)j, q.w, q.y, {0, 0}};
+            if (q.w <= 1) continue;
+            for (int64_t j = 1 + lane; j < q.w; j += 64) put(a, q, base + i, j);
         }
         carry += total;
     }
@@ -64,6 +70,7 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
     if (tid == 0) {
         a.words[0] = s_bad;
         a.words[1] = 0;
+        a.words[2] = (int)min(carry, a.max_tiles);
     }
 }
 
