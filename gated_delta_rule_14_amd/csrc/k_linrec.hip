@@ -355,9 +355,13 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
         s_A[s.w][s.lane * V + e] = A[e];
         s_H[s.w][s.lane * V + e] = H[e];
     }
+    float h[V];
+    if constexpr (!HAND) {   // read by every wave before one of them may write ht, which may be h0
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[e] = p.h0 ? p.h0[t.seq * p.D + s.c + e] : 0.f;
+    }
     __syncthreads();
     const int tid = threadIdx.x;
-    float h[V];
     if constexpr (HAND) {
         const int part = s.w * 64 / CB, k = tid - part * CB;      // the same part for the whole wave
         const bool own = part == 0 && c0 + k < p.D;
@@ -389,9 +393,6 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
         if (!p.y) return;
 #pragma unroll
         for (int e = 0; e < V; ++e) h[e] = entering<CB>(s_pA, s_pH, s.lane * V + e);
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = p.h0 ? p.h0[t.seq * p.D + s.c + e] : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < V; ++e)

@@ -142,6 +142,21 @@ def test_step_sizes(gpu_lib, D, dt):
         ref.check(d["h0"], want["ht"], err["ht"], "state")
 
 
+@pytest.mark.parametrize("T", [3, 16, 40, 64, 100, 300])
+@pytest.mark.parametrize("packed", [False, True])
+def test_final_state_over_the_initial_one(gpu_lib, T, packed):
+    """ht may be h0: sequences of one wave, of several, of several tiles; the waves of a sequence all read
+    h0, one of them writes ht, and with many sequences they do not run in step."""
+    print("case: linrec ht = h0", T, packed, flush=True)
+    N, D = 200, 130
+    d = inputs(51 + T, 1 if packed else N, N * T if packed else T, D, N=N)
+    cu = torch.arange(0, N * T + 1, T).cuda() if packed else None
+    y, ht = gpu_lib.linrec_fwd(d["x"], d["g"], h0=d["h0"], cu_seqlens=cu)
+    state = d["h0"].clone()
+    y2, ht2 = gpu_lib.linrec_fwd(d["x"], d["g"], h0=state, cu_seqlens=cu, ht=state)
+    assert ht2 is state and torch.equal(ht, state) and torch.equal(y, y2)
+
+
 def test_state_in_place_and_empty(gpu_lib):
     """ht may be h0; sequences without tokens keep their state, also with T = 0."""
     gdn = gpu_lib
