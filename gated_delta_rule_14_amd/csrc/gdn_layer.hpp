@@ -138,6 +138,7 @@ struct LinrecLaunch {
     double* sums = nullptr;       // shares of the sums of part
     // hand-offs between the tiles of a sequence; nullptr where every sequence is one tile
     uint64_t *pairs = nullptr, *groups = nullptr;   // [max_tiles][D], [max_tiles / 16 + 1][D]
+    bool keep_status = false;     // clear: words[1] is already this call's
     int* words = nullptr;         // check of the offsets, failed waits, table rows in use; [TICKET]
     int64_t D = 0, xs = 0, gs = 0, ys = 0;   // channels; token strides of x, g, y / dy
     bool x_bf16 = false, g_bf16 = false;

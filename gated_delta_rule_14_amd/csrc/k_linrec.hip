@@ -150,7 +150,7 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* row, unsigned off) {
 
 // Compose the pairs of channel c in rows p, p + step, ... (n of them; p, step and n the same
 // for the whole wave) in that order onto (A, H), 8 loads in flight at once.  `polls`: what
-// is left of this thread's patience; 0 once a wait gave up.
+// is left of this thread's patience; 0 or less once a wait gave up.
 __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, int64_t c, float* A, float* H,
                                         int* polls, const int* failed) {
     constexpr int U = GROUP / 2;
@@ -197,7 +197,7 @@ __device__ __forceinline__ void enter_own(const LinrecLaunch& p, int64_t tile, i
     compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls, p.words + 1);
     if (part == 0 && j == 0) *H = start;
     if (part == 0 && j < GROUP) *A = 0.f;          // a value, whatever the A of the pairs after the first
-    if (polls == 0) atomicExch(p.words + 1, 1);
+    if (polls <= 0) atomicExch(p.words + 1, 1);
 }
 // part 2 or 3
 __device__ __forceinline__ void enter_groups(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
@@ -210,7 +210,7 @@ __device__ __forceinline__ void enter_groups(const LinrecLaunch& p, int64_t tile
     *H = 0.f;
     compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls, p.words + 1);
     if (part == 2 && ng > 0) *A = 0.f;
-    if (polls == 0) atomicExch(p.words + 1, 1);
+    if (polls <= 0) atomicExch(p.words + 1, 1);
 }
 // the tile's own pair; and once the parts of its group are there, the group's
 __device__ __forceinline__ void publish_tile(const LinrecLaunch& p, int64_t tile, int j, int nt, int64_t c, float A,
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(256) void linrec_clear_kernel(LinrecLaunch p, const
     const int64_t c0 = (int64_t)(blockIdx.x - i * nb) * 512 + threadIdx.x;
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.pairs) {
         if (!p.map.table) p.words[0] = 0;
-        p.words[1] = 0;
+        if (!p.keep_status) p.words[1] = 0;
         p.words[TICKET] = 0;
     }
     const int64_t tiles = p.pairs ? p.map.max_tiles : 0;
@@ -748,7 +748,9 @@ hipError_t launch_linrec_bwd(const LinrecLaunch& p) {
         f.ht = nullptr;
         if ((e = launch_linrec_fwd(f)) != hipSuccess) return e;
     }
-    if ((e = clear(p, p.dht, p.dh0)) != hipSuccess) return e;
+    LinrecLaunch c = p;
+    c.keep_status = p.own_states && !p.small;        // of the states' waits
+    if ((e = clear(c, p.dht, p.dh0)) != hipSuccess) return e;
     if (p.map.T > 0) {
         if (p.small) e = bwd_few(p, p.small);
         else if (!p.shorts || (e = bwd_few(short_ones(p), p.shorts)) == hipSuccess) e = go<BWD>(p);

@@ -281,6 +281,25 @@ def test_supplied_outputs_and_workspace(gpu_lib):
     assert b["dh0"] is None and gdn.linrec_fwd(d["x"], d["g"], output_final_state=False)[1] is None
 
 
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("packed", [False, True])
+def test_status_words(gpu_lib, keep, packed):
+    """The two status words are this call's, whatever the workspace held."""
+    print("case: linrec status words", keep, packed, flush=True)
+    d = inputs(23, 1 if packed else 2, 2300, 40)
+    cu = torch.tensor([0, 300, 2300]).cuda() if packed else None
+    h0 = torch.zeros(2, 40, device="cuda")
+    states = gpu_lib.linrec_states(d["x"], cu) if keep else None
+    ws = torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")
+    gpu_lib.linrec_fwd(d["x"], d["g"], h0=h0, cu_seqlens=cu, states=states, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws[:8].view(torch.int32).tolist() == [0, 0]
+    ws.fill_(255)
+    gpu_lib.linrec_bwd(d["x"], d["g"], d["dy"], h0=h0, cu_seqlens=cu, states=states, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws[:8].view(torch.int32).tolist() == [0, 0]
+
+
 def test_gradient_against_differences(gpu_lib):
     """A directional difference of the kernel's own float32 forward."""
     gdn = gpu_lib
