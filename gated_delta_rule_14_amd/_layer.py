@@ -357,7 +357,7 @@ def _qk(q, k, inv_freq, positions, norm, eps, q_weight, k_weight, weight_offset,
         _dense(k_weight, "k_weight", (D,), dev)
     (qt, qh), (kt, kh) = _heads(q, "q"), _heads(k, "k")
     return _qk_plan(B, T, Hq, ks[2], D, R, qt, kt, qh, kh, _code(q, "q"), NORMS[norm],
-                    QK_INTERLEAVED if interleaved else 0, eps, weight_offset), dev, qs, ks
+                    QK_INTERLEAVED if interleaved else 0, float(eps), float(weight_offset)), dev, qs, ks
 
 
 def qk_norm_rope(q, k, inv_freq=None, positions=None, norm="l2", eps=1e-6, q_weight=None, k_weight=None,

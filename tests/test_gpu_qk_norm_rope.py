@@ -148,6 +148,20 @@ def test_same_bits_streams_and_graphs(gpu_lib):
         assert all(torch.equal(want[n], out[n]) for n in want), i
 
 
+def test_options_are_read_at_every_call(gpu_lib):
+    """eps and weight_offset as scalars that change between two calls."""
+    d = inputs(61, 1, 5, 2, 2, 64)
+    eps, offset = torch.tensor(1e-6), torch.tensor(0.0)
+    kw = dict(norm="rms", q_weight=d["qw"])
+    for e, o in ((1e-6, 0.0), (0.5, 1.0)):
+        eps.fill_(e)
+        offset.fill_(o)
+        got = gpu_lib.qk_norm_rope(d["q"], d["k"], eps=eps, weight_offset=offset, **kw)
+        want = gpu_lib.qk_norm_rope(d["q"], d["k"], eps=e, weight_offset=o, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (e, o)
+
+
 def test_refusals(gpu_lib):
     gdn = gpu_lib
     q, k, f = torch.zeros(1, 4, 4, 64, device="cuda"), torch.zeros(1, 4, 2, 64, device="cuda"), freqs(64)
