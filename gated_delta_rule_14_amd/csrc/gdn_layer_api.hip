@@ -179,7 +179,8 @@ LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
 // the grids of the tiles, the hand-offs' clearing, the empty sequences and the parameter sums
 gdn_status check_linrec_grid(const gdn_linrec_desc* d, const LinrecLayout& L) {
     const double D = (double)d->channels, N = (double)(d->num_seqs > 0 ? d->num_seqs : d->batch);
-    gdn_status s = check_grid((double)L.t.tiles * ((D + 63) / 64), 1024);
+    const double threads = L.small == 16 ? 128 : L.small == 64 ? 512 : 1024;
+    gdn_status s = check_grid((double)L.t.tiles * ((D + 63) / 64), threads);
     if (s == GDN_OK && L.shorts) s = check_grid(N * ((D + 63) / 64), 512);
     if (s == GDN_OK) s = check_grid((N + (double)L.t.tiles) * ((D + 511) / 512), 256);
     return s != GDN_OK ? s : check_grid(2 * ((D + 15) / 16), 1024);

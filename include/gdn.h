@@ -499,7 +499,9 @@ gdn_status gdn_chunk_bwd_act(const gdn_fwd_desc *d, const gdn_activation *act,
  *   u_t = x_t, or sqrt(1 - a_t^2) x_t with GDN_LINREC_NORMALIZE (g <= 0 then).
  * With act (flags GDN_ACT_GATE or 0; other flags give GDN_ERR_UNSUPPORTED) g
  * holds raw logits and log a = -exp(A_log[c]) softplus(g + dt_bias[c]), A_log
- * and dt_bias [D] float.  The state is kept in fp32.
+ * and dt_bias [D] float.  The state is kept in fp32.  Decays (g <= 0) are
+ * meant: the kernels form products of a over stretches of up to 2048 tokens,
+ * so growing gates need these products finite, not the states alone.
  */
 enum { GDN_LINREC_NORMALIZE = 1 };
 typedef struct gdn_linrec_desc {

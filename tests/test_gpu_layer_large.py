@@ -101,3 +101,27 @@ def test_two_calls_at_once(gpu_lib):
     for r in got:
         for a, b in zip(r, want):
             assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_many_single_tokens(gpu_lib):
+    """More sequences of one token than a launch has tiles of a whole workgroup."""
+    N, D = 70000, 4096
+    x = torch.randn(N, 1, D, device="cuda", dtype=torch.bfloat16)
+    g = torch.full((N, 1, D), -0.5, device="cuda")
+    h0 = torch.randn(N, D, device="cuda")
+    print("case: linrec", N, 1, D, flush=True)
+    y, ht = gpu_lib.linrec_fwd(x, g, h0=h0)
+    out = gpu_lib.linrec_bwd(x, g, x, h0=h0, dht=h0)
+    step = h0.clone()
+    gpu_lib.linrec_step(x[:, 0], g[:, 0], step)
+    torch.cuda.synchronize()
+    assert torch.equal(ht, step)                    # the same product and sum, rounded once each or fused in both
+    for n in (0, N // 2, N - 1):
+        a, h, v = torch.exp(torch.tensor(-0.5, dtype=torch.float64)), h0[n].double().cpu(), x[n, 0].double().cpu()
+        want = a * h + v
+        # two products or sums of 2^-23 and an a off by a few of them, then the output's half step
+        tol = 2.0 ** -20 * (a * h).abs() + 2.0 ** -22 * want.abs() + 1e-30
+        assert ((ht[n].double().cpu() - want).abs() <= tol).all()
+        assert ((y[n, 0].double().cpu() - want).abs() <= tol + 2.0 ** -8 * want.abs()).all()
+        dh = v + h
+        assert ((out["dh0"][n].double().cpu() - a * dh).abs() <= 2.0 ** -20 * (v.abs() + h.abs())).all()
