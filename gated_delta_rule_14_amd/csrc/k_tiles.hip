@@ -78,7 +78,10 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
 // column, 8 loads of a strand in flight, met in LDS.  With many rows and few
 // columns the rows are shared out over a.shares workgroups and their sums
 // added by a second launch: one workgroup per 64 columns would leave most of
-// the chip idle (4103 rows of 256 columns: 28 us by 16 workgroups).
+// the chip idle (4103 rows of 256 columns: 28 us by 16 workgroups; of a backward
+// with 2559 rows of 8192 columns it saves 25 us of 314).  Where the columns
+// are many, the second launch costs more than it saves (627 rows of 20480 columns:
+// 130 -> 162 us).
 template <bool LAST>
 __global__ __launch_bounds__(1024) void row_sum_kernel(RowSumLaunch a) {
     __shared__ double s[16][64];
@@ -118,7 +121,7 @@ __global__ __launch_bounds__(1024) void row_sum_kernel(RowSumLaunch a) {
     }
 }
 
-int64_t row_sum_shares(int64_t rows, int64_t cols) { return cols < 8192 && rows > 512 ? 32 : 1; }
+int64_t row_sum_shares(int64_t rows, int64_t cols) { return rows > 512 && rows > cols / 8 ? 32 : 1; }
 
 hipError_t launch_row_sum(const RowSumLaunch& in) {
     RowSumLaunch a = in;
