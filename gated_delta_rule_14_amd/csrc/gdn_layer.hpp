@@ -116,6 +116,8 @@ struct RowSumLaunch {
     double* sums;                 // [shares][count][D], used where shares > 1
     hipStream_t stream;
     int64_t shares = 1;           // set by the launch
+    const int* used = nullptr;    // or the last `most` rows are only so many (a device word)
+    int64_t most = 0;
 };
 int64_t row_sum_shares(int64_t rows, int64_t cols);
 hipError_t launch_row_sum(const RowSumLaunch& a);
@@ -134,7 +136,7 @@ struct LinrecLaunch {
     int small = 0, shorts = 0;
     float* states = nullptr;      // [max_tiles][D] the states entering the tiles
     bool own_states = false;      // backward: states is workspace, to be filled first
-    float* part = nullptr;        // [max_tiles, then N with shorts][2][D] sums of dA_log and ddt_bias (backward)
+    float* part = nullptr;        // [N with shorts, then max_tiles][2][D] sums of dA_log and ddt_bias (backward)
     double* sums = nullptr;       // shares of the sums of part
     // hand-offs between the tiles of a sequence; nullptr where every sequence is one tile
     uint64_t *pairs = nullptr, *groups = nullptr;   // [max_tiles][D], [max_tiles / 16 + 1][D]

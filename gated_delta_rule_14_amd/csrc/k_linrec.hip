@@ -34,6 +34,8 @@
 // tokens and 128 channels, 16 tokens to a wave: tiles of 64 tokens take 15 to
 // 35 % longer (a hand-off for half the work), of 256 leave one workgroup to a
 // CU, 8 % longer on the packed input.
+#include <algorithm>
+
 #include "gdn_layer.hpp"
 
 namespace gdn {
@@ -260,23 +262,26 @@ __global__ __launch_bounds__(256) void linrec_clear_kernel(LinrecLaunch p, const
 
 // Tile and channel block of this workgroup (of nb blocks): by ticket where tiles
 // wait for each other.  With sequences that run without hand-offs most rows of
-// the table may be unused, and those, its last, need no ticket (one counter
-// serves 87 million a second); else the word that says so is not waited for.
-template <bool HAND>
-__device__ __forceinline__ unsigned tile_by_ticket(const LinrecLaunch& p, unsigned nb, bool backward, unsigned* block,
-                                                   unsigned* s) {
+// the table may be unused: then the chip's fill of workgroups takes tickets
+// until the rows in use are done (a workgroup to each row: 54 us for 2559 unused
+// ones).  Else the word that tells the rows in use is not waited for.
+// False: none left.
+constexpr int64_t FILL = 512;
+enum { ALONE, TILES, QUEUE };   // HAND: without hand-offs, with, and with them row after row
+template <int HAND>
+__device__ __forceinline__ bool tile_by_ticket(const LinrecLaunch& p, unsigned nb, bool backward, unsigned* tile,
+                                               unsigned* block, unsigned* s) {
     unsigned k = blockIdx.x, used = (unsigned)p.map.max_tiles;
     if (HAND && p.pairs) {                 // else every sequence is one tile: no words
-        if (p.shorts) used = __builtin_amdgcn_readfirstlane((unsigned)p.words[2]);
-        if (k < used * nb) {
-            if (threadIdx.x == 0) *s = atomicAdd(reinterpret_cast<unsigned*>(p.words) + TICKET, 1u);
-            __syncthreads();
-            k = __builtin_amdgcn_readfirstlane(*s);
-        }
+        if (HAND == QUEUE) used = __builtin_amdgcn_readfirstlane((unsigned)p.words[2]);
+        if (threadIdx.x == 0) *s = atomicAdd(reinterpret_cast<unsigned*>(p.words) + TICKET, 1u);
+        __syncthreads();
+        k = __builtin_amdgcn_readfirstlane(*s);
     }
     const unsigned i = k / nb;
     *block = k - i * nb;
-    return HAND && backward && i < used ? used - 1 - i : i;
+    *tile = HAND && backward ? used - 1 - i : i;
+    return HAND != QUEUE || i < used;
 }
 
 // A wave's place in its tile.
@@ -308,7 +313,7 @@ __device__ __forceinline__ const T* row_at(const T* tile, int64_t stride, const 
 }
 
 // HAND: tiles of a sequence hand their pairs on; without it every sequence is one tile.
-template <bool FULL, bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <bool FULL, int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_pA)[64 * V],
                                          float (*s_pH)[64 * V]) {
@@ -413,19 +418,23 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
     }
 }
 
-template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
     static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
     __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[HAND ? NT : 1][CB], s_pH[HAND ? NT : 1][CB];
     __shared__ unsigned s_ticket;
-    unsigned block;
-    const unsigned tile = tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), false, &block, &s_ticket);
-    const int64_t c0 = (int64_t)block * CB;
-    const Tile t = tile_of(p.map, tile);
-    if (t.n <= 0) return;
-    if (t.n == S * NW) fwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
-    else fwd_tile<false, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
+    unsigned tile, block;
+    while (tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), false, &tile, &block, &s_ticket)) {
+        const int64_t c0 = (int64_t)block * CB;
+        const Tile t = tile_of(p.map, tile);
+        if (HAND != QUEUE && t.n <= 0) return;
+        if (t.n == S * NW) fwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
+        else if (HAND != QUEUE || t.n > 0)
+            fwd_tile<false, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_pA, s_pH);
+        if (HAND != QUEUE) return;
+        __syncthreads();                       // the waves are done with the tile's LDS
+    }
 }
 
 // The same tiles taken from the last token: e = a (dy + e') is what a token
@@ -436,7 +445,7 @@ __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) 
 // channels, bf16, raw gates, normalised: 116 us against 66 us of bytes and 73
 // us of ALU slots; one workgroup fills a CU, so the loads and the hand-off of
 // a tile are not hidden by another.
-template <bool FULL, bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <bool FULL, int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_E)[64 * V],
                                          float (*s_pA)[64 * V], float (*s_pE)[64 * V], float* s_in,
@@ -612,7 +621,7 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
     }
 }
 
-template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
     static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
@@ -622,20 +631,25 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     // the end, and next to a, m, x and dy there are no registers for them
     __shared__ f32x2v s_gate[ACT ? S * V : 1][64 * NW];
     __shared__ unsigned s_ticket;
-    unsigned block;
-    const unsigned tile = tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), true, &block, &s_ticket);
-    const int64_t c0 = (int64_t)block * CB;
-    const Tile t = tile_of(p.map, tile);
-    if (t.n <= 0) {
-        if (ACT)
-            for (int k = threadIdx.x; k < CB && c0 + k < p.D; k += 64 * NW) {
-                p.part[(int64_t)(2 * tile) * p.D + c0 + k] = 0.f;
-                p.part[(int64_t)(2 * tile + 1) * p.D + c0 + k] = 0.f;
-            }
-        return;
+    unsigned tile, block;
+    while (tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), true, &tile, &block, &s_ticket)) {
+        const int64_t c0 = (int64_t)block * CB;
+        const Tile t = tile_of(p.map, tile);
+        if (t.n <= 0) {
+            if (ACT)
+                for (int k = threadIdx.x; k < CB && c0 + k < p.D; k += 64 * NW) {
+                    p.part[(int64_t)(2 * tile) * p.D + c0 + k] = 0.f;
+                    p.part[(int64_t)(2 * tile + 1) * p.D + c0 + k] = 0.f;
+                }
+            if (HAND != QUEUE) return;
+        } else if (t.n == S * NW) {
+            bwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
+        } else {
+            bwd_tile<false, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
+        }
+        if (HAND != QUEUE) return;
+        __syncthreads();                       // the waves are done with the tile's LDS
     }
-    if (t.n == S * NW) bwd_tile<true, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
-    else bwd_tile<false, HAND, X, G, ACT, NORM, V, S, NW>(p, t, tile, c0, s_A, s_H, s_E, s_pA, s_pE, s_in, s_gate);
 }
 
 // One token: y and the state, in place.  32 x 2048 takes 3 us, the time of a launch.
@@ -663,13 +677,13 @@ __global__ __launch_bounds__(64) void linrec_step_kernel(LinrecLaunch p) {
 }
 
 // ---- launches
-enum { FWD, FWD16, FWD64, BWD, BWD16, BWD64, STEP };
-template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+enum { FWD, FWDQ, FWD16, FWD64, BWD, BWDQ, BWD16, BWD64, STEP };
+template <int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 static void fwd(const LinrecLaunch& p, int64_t blocks) {
     hipLaunchKernelGGL((linrec_fwd_kernel<HAND, X, G, ACT, NORM, V, S, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0,
                        p.stream, p);
 }
-template <bool HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
+template <int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 static void bwd(const LinrecLaunch& p, int64_t blocks) {
     hipLaunchKernelGGL((linrec_bwd_kernel<HAND, X, G, ACT, NORM, V, S, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0,
                        p.stream, p);
@@ -677,12 +691,14 @@ static void bwd(const LinrecLaunch& p, int64_t blocks) {
 template <int WHICH, typename X, typename G, bool ACT, bool NORM, int V>
 static hipError_t go2(const LinrecLaunch& p) {
     const int64_t nb = (p.D + 64 * V - 1) / (64 * V), tiles = nb * (p.map.shorts ? p.map.N : p.map.max_tiles);
-    if constexpr (WHICH == FWD) fwd<true, X, G, ACT, NORM, V, 16, 8>(p, tiles);
-    else if constexpr (WHICH == FWD16) fwd<false, X, G, ACT, NORM, V, 16, 1>(p, tiles);
-    else if constexpr (WHICH == FWD64) fwd<false, X, G, ACT, NORM, V, 16, 4>(p, tiles);
-    else if constexpr (WHICH == BWD) bwd<true, X, G, ACT, NORM, V, 8, 16>(p, tiles);
-    else if constexpr (WHICH == BWD16) bwd<false, X, G, ACT, NORM, V, 8, 2>(p, tiles);
-    else if constexpr (WHICH == BWD64) bwd<false, X, G, ACT, NORM, V, 8, 8>(p, tiles);
+    if constexpr (WHICH == FWD) fwd<TILES, X, G, ACT, NORM, V, 16, 8>(p, tiles);
+    else if constexpr (WHICH == FWDQ) fwd<QUEUE, X, G, ACT, NORM, V, 16, 8>(p, std::min(tiles, FILL));
+    else if constexpr (WHICH == FWD16) fwd<ALONE, X, G, ACT, NORM, V, 16, 1>(p, tiles);
+    else if constexpr (WHICH == FWD64) fwd<ALONE, X, G, ACT, NORM, V, 16, 4>(p, tiles);
+    else if constexpr (WHICH == BWD) bwd<TILES, X, G, ACT, NORM, V, 8, 16>(p, tiles);
+    else if constexpr (WHICH == BWDQ) bwd<QUEUE, X, G, ACT, NORM, V, 8, 16>(p, std::min(tiles, FILL));
+    else if constexpr (WHICH == BWD16) bwd<ALONE, X, G, ACT, NORM, V, 8, 2>(p, tiles);
+    else if constexpr (WHICH == BWD64) bwd<ALONE, X, G, ACT, NORM, V, 8, 8>(p, tiles);
     else
         hipLaunchKernelGGL((linrec_step_kernel<X, G, ACT, NORM, V>), dim3((unsigned)(nb * p.map.N)), dim3(64), 0,
                            p.stream, p);
@@ -726,7 +742,6 @@ static LinrecLaunch short_ones(const LinrecLaunch& p) {
     LinrecLaunch q = p;
     q.map.shorts = p.shorts;
     q.states = nullptr;
-    if (q.part) q.part += 2 * p.map.max_tiles * p.D;
     return q;
 }
 static hipError_t fwd_few(const LinrecLaunch& p, int few) { return few == 16 ? go<FWD16>(p) : go<FWD64>(p); }
@@ -737,7 +752,7 @@ hipError_t launch_linrec_fwd(const LinrecLaunch& p) {
     if (e != hipSuccess || p.map.T == 0) return e;
     if (p.small) return fwd_few(p, p.small);
     if (p.shorts && (p.y || p.ht) && (e = fwd_few(short_ones(p), p.shorts)) != hipSuccess) return e;
-    return go<FWD>(p);
+    return p.shorts ? go<FWDQ>(p) : go<FWD>(p);
 }
 
 hipError_t launch_linrec_bwd(const LinrecLaunch& p) {
@@ -750,15 +765,18 @@ hipError_t launch_linrec_bwd(const LinrecLaunch& p) {
     }
     LinrecLaunch c = p;
     c.keep_status = p.own_states && !p.small;        // of the states' waits
+    if (p.shorts) c.part += 2 * p.map.N * p.D;
     if ((e = clear(c, p.dht, p.dh0)) != hipSuccess) return e;
     if (p.map.T > 0) {
         if (p.small) e = bwd_few(p, p.small);
-        else if (!p.shorts || (e = bwd_few(short_ones(p), p.shorts)) == hipSuccess) e = go<BWD>(p);
+        else if (p.shorts && (e = bwd_few(short_ones(p), p.shorts)) != hipSuccess) return e;
+        else e = p.shorts ? go<BWDQ>(c) : go<BWD>(c);
         if (e != hipSuccess) return e;
     }
     if (!(p.act.flags & ACT_GATE)) return hipSuccess;
     const int64_t rows = p.map.T > 0 ? p.map.max_tiles + (p.shorts ? p.map.N : 0) : 0;
-    return launch_row_sum(RowSumLaunch{p.part, rows, p.D, 1, 2, p.dA_log, p.ddt_bias, p.sums, p.stream});
+    return launch_row_sum(RowSumLaunch{p.part, rows, p.D, 1, 2, p.dA_log, p.ddt_bias, p.sums, p.stream, 1,
+                                       p.shorts ? p.words + 2 : nullptr, p.map.max_tiles});
 }
 
 hipError_t launch_linrec_step(const LinrecLaunch& p) { return go<STEP>(p); }

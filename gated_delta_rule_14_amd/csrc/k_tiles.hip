@@ -58,9 +58,10 @@ __global__ __launch_bounds__(1024) void tile_table_kernel(TileTableLaunch a) {
         if (n < a.N) a.seqs[n] = make_int4((int)s, (int)len, (int)first, 0);
         __syncthreads();
         if (n < a.N && s_seq[tid].w > 0) put(a, s_seq[tid], n, 0);
-        for (int i = wave; i < 1024 && base + i < a.N; i += 16) {
+        const int mine = wave + 16 * lane;             // the wave's sequences are every 16th
+        for (uint64_t m = __ballot(base + mine < a.N && s_seq[mine].w > 1); m; m &= m - 1) {
+            const int i = wave + 16 * (__ffsll((unsigned long long)m) - 1);
             const int4 q = s_seq[i];
-            if (q.w <= 1) continue;
             for (int64_t j = 1 + lane; j < q.w; j += 64) put(a, q, base + i, j);
         }
         carry += total;
@@ -94,7 +95,8 @@ __global__ __launch_bounds__(1024) void row_sum_kernel(RowSumLaunch a) {
         if (LAST && a.shares > 1) {
             for (int64_t i = strand; i < a.shares; i += 16) v += a.sums[i * cols + col];
         } else {
-            const int64_t per = (a.rows + a.shares - 1) / a.shares, end = min(a.rows, (share + 1) * per);
+            const int64_t rows = a.used ? a.rows - a.most + *a.used : a.rows;
+            const int64_t per = (rows + a.shares - 1) / a.shares, end = min(rows, (share + 1) * per);
             const float* p = a.part + col;
             for (int64_t i = share * per + strand; i < end; i += 8 * 16) {
                 float x[8];

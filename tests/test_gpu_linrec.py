@@ -96,6 +96,33 @@ def short_among_long(gpu_lib, D, lengths):
     both(gpu_lib, inputs(26, 1, T, D, F32, F32, N=N), cu)
 
 
+def test_many_tiles_among_short_sequences(gpu_lib):
+    """More tiles and channel blocks in use than workgroups that take them in turn: repeated columns
+    have to give the columns' own result."""
+    lengths = [2] * 3000 + [2500] * 10 + [3] * 500 + [129] * 10
+    T, N, R = sum(lengths), len(lengths), 16
+    cu = torch.tensor([0] + lengths).cumsum(0).cuda()
+    print("case: linrec tiles in turn", T, N, 64 * R, flush=True)
+    d = inputs(71, 1, T, 64, BF, BF, True, N=N)
+
+    def call(r):
+        w = {k: v.repeat(*([1] * (v.dim() - 1)), r) for k, v in d.items()}
+        gate = dict(h0=w["h0"], cu_seqlens=cu, normalize=True, A_log=w["A_log"], dt_bias=w["dt_bias"])
+        y, ht = gpu_lib.linrec_fwd(w["x"], w["g"], **gate)
+        out = gpu_lib.linrec_bwd(w["x"], w["g"], w["dy"], dht=w["dht"], **gate)
+        torch.cuda.synchronize()
+        return dict(out, y=y, ht=ht)
+    one, many = call(1), call(R)
+    for n, v in one.items():
+        assert torch.equal(v.repeat(*([1] * (v.dim() - 1)), R), many[n]), n
+    for i in (0, 2999, 3000, 3009, 3010, 3519):        # first and last of each kind, by the call of it alone
+        a, b = int(cu[i]), int(cu[i + 1])
+        y, ht = gpu_lib.linrec_fwd(d["x"][:, a:b].contiguous(), d["g"][:, a:b].contiguous(), h0=d["h0"][i:i + 1].contiguous(),
+                                   normalize=True, A_log=d["A_log"], dt_bias=d["dt_bias"])
+        torch.cuda.synchronize()
+        assert torch.equal(y, one["y"][:, a:b]) and torch.equal(ht, one["ht"][i:i + 1]), i
+
+
 def test_long_sequence(gpu_lib):
     """More tiles than one group of the look-back."""
     print("case: linrec long", flush=True)
