@@ -10,7 +10,7 @@
 //
 // Measured (bf16): 4 x 4096 tokens of 16 + 16 heads of 128, 45 us, 6.0 TB/s
 // with part of it in the cache; 16411 tokens of 32 + 8 heads, 67 us forward
-// (5.0 TB/s, a large copy's rate) and 120 us backward (4.2 TB/s); 64 tokens of
+// (5.0 TB/s, a large copy's rate) and 115 us backward (4.4 TB/s); 64 tokens of
 // 16 + 2 heads of 256, 4.8 us.
 //
 // The element that a half-split rotation pairs with sits R/16 lanes away and
