@@ -292,6 +292,38 @@ def test_same_bits_streams_and_graphs(gpu_lib, monkeypatch):
             assert all(torch.equal(want[n], out[n]) for n in want), k
 
 
+def test_packed_short_sequences_in_a_graph(gpu_lib, monkeypatch):
+    """Captured and replayed on other inputs, with eager calls between the replays, and on two streams at once."""
+    monkeypatch.setenv("GDN_DEBUG", "0")        # its check of the words synchronises
+    lengths = [2] * 300 + [700, 0, 2500, 64] * 3
+    T, N = sum(lengths), len(lengths)
+    cu = torch.tensor([0] + lengths).cumsum(0).cuda()
+    print("case: linrec short packed graph", T, N, flush=True)
+    d = inputs(81, 1, T, 130, BF, BF, True, N=N)
+    kw = dict(h0=d["h0"], cu_seqlens=cu, normalize=True, A_log=d["A_log"], dt_bias=d["dt_bias"])
+
+    def call(stream=None):
+        y, ht = gpu_lib.linrec_fwd(d["x"], d["g"], stream=stream, **kw)
+        return dict(gpu_lib.linrec_bwd(d["x"], d["g"], d["dy"], dht=d["dht"], stream=stream, **kw), y=y, ht=ht)
+    first = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [call(s) for _ in range(3) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first[n], o[n]) for o in outs for n in first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    x0 = d["x"].clone()
+    for i in range(4):
+        d["x"].copy_(x0 * (1 + i))
+        want = call()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[n], out[n]) for n in want), i
+
+
 def test_supplied_outputs_and_workspace(gpu_lib):
     gdn = gpu_lib
     d = inputs(22, 2, 150, 40)
