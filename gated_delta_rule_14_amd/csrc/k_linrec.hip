@@ -11,13 +11,17 @@
 //
 // The pairs are published without waiting for anything, so a tile waits for
 // one hand-off only, not for a chain of them.  Sixteen tiles form a group whose last
-// tile publishes the group's pair too (after reading the other fifteen): a
-// tile reads at most 15 pairs of its own group and one of every group before.  They are
-// composed in the order of the tokens, whatever order they arrive in, so
-// equal calls give equal bits.  A pair is one 64-bit word, stored and loaded
-// by relaxed agent-scope atomics: it is there whole or not at all, so no
-// fence and no flag is needed; "not there" is a NaN pattern of A that is
-// never published, set by a kernel in front.
+// tile publishes the group's pair too (after reading the other fifteen), and
+// later, in its place, the state that leaves the group.  A tile reads at most
+// 15 pairs of its own group, and the groups before from a late one on whose
+// state is there, so that the reads do not grow with the sequence (1048576 tokens
+// of 512 channels, bf16 with raw gates: forward 1.54 -> 0.85 ms next to reading
+// all of them).  Groups are applied to a state, one after the other:
+// products of a never span more than a group, 2048 tokens, and where a tile
+// starts does not change what is computed, so equal calls give equal bits.  A pair is one
+// 64-bit word, stored and loaded by relaxed agent-scope atomics: it is there
+// whole or not at all, so no fence and no flag is needed; "not there" is a NaN
+// pattern of A that is never published, set by a kernel in front.
 //
 // Workgroups take their tile from a ticket counter, tiles in the order they
 // wait for each other, the channel blocks of a tile one after the other (a
@@ -42,6 +46,7 @@ namespace gdn {
 
 constexpr int GROUP = 16;
 constexpr unsigned ABSENT = 0xffffffffu;     // never the bits of a published A
+constexpr unsigned STATE = 0x80000000u;      // -0, which no product of a is: H is the state itself
 constexpr int POLLS = 1 << 20;               // about a second; a hand-off takes microseconds
 
 // ---- gates
@@ -145,17 +150,19 @@ __device__ __forceinline__ void publish(uint64_t* p, float A, float H) {
     const unsigned a = A != A ? 0x7fc00000u : __float_as_uint(A);
     __hip_atomic_store(p, (uint64_t)__float_as_uint(H) << 32 | a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void publish_state(uint64_t* p, float H) { publish(p, __uint_as_float(STATE), H); }
 __device__ __forceinline__ uint64_t peek(const uint64_t* row, unsigned off) {
     return __hip_atomic_load((const GDN_GLOBAL uint64_t*)((const GDN_GLOBAL char*)in_scalar(row) + off),
                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+constexpr int BATCH = 8;
 // Compose the pairs of channel c in rows p, p + step, ... (n of them; p, step and n the same
 // for the whole wave) in that order onto (A, H), 8 loads in flight at once.  `polls`: what
 // is left of this thread's patience; 0 or less once a wait gave up.
 __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, int64_t c, float* A, float* H,
                                         int* polls, const int* failed) {
-    constexpr int U = GROUP / 2;
+    constexpr int U = BATCH;
     const unsigned off = (unsigned)c * 8;
     for (int i = 0; i < n; i += U) {
         uint64_t v[U];
@@ -171,24 +178,26 @@ __device__ __forceinline__ void compose(const uint64_t* p, int64_t step, int n, 
             if (missing && *polls % 1024 == 1 && __hip_atomic_load(failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
                 *polls = 1;
         } while (missing && --*polls > 0);
+        // (a STATE by its sign, which no other word has by now: a comparison with the pattern is
+        // moved into the loop above and costs 16 registers)
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const bool past = i + k >= n;
-            const float a = past ? 1.f : __uint_as_float((unsigned)v[k]);
-            *H = a * *H + (past ? 0.f : __uint_as_float((unsigned)(v[k] >> 32)));
-            *A *= a;
+            const float a = __uint_as_float((unsigned)v[k]), h = __uint_as_float((unsigned)(v[k] >> 32));
+            *H = past ? *H : (int)(unsigned)v[k] < 0 ? h : __builtin_fmaf(a, *H, h);
+            *A = past ? *A : *A * a;
         }
     }
 }
 
 // What enters tile j of a sequence (of nt; row `tile` of the workspace) is put
 // together from the pairs of the tiles and groups before it by NT threads to
-// a channel: two halves of its own group's tiles (parts 0, 1), two of the
-// groups before (parts 2, 3), all waited for at once.  dir = 1: tiles in the
+// a channel: two halves of its own group's tiles (parts 0, 1) and the groups
+// before (part 2), all waited for at once.  dir = 1: tiles in the
 // order of the tokens; -1: against it, j counted from the sequence's end.
-// The first tile's pair, and its group's, are published as (0, value) with
-// the value that enters the sequence worked in: composing onto anything gives that value.
-constexpr int NT = 4;
+// The first tile publishes a state, with the value that enters the sequence
+// worked in, and so does the first group.
+constexpr int NT = 3;
 // part 0 or 1; start: the value that enters the sequence
 __device__ __forceinline__ void enter_own(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
                                           float start, float* A, float* H) {
@@ -198,39 +207,56 @@ __device__ __forceinline__ void enter_own(const LinrecLaunch& p, int64_t tile, i
     *H = 0.f;
     compose(p.pairs + (tile + (int64_t)dir * (s0 - in)) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls, p.words + 1);
     if (part == 0 && j == 0) *H = start;
-    if (part == 0 && j < GROUP) *A = 0.f;          // a value, whatever the A of the pairs after the first
+    if (part == 0 && j < GROUP) *A = 0.f;          // a state, whatever the A of the pairs after the first
     if (polls <= 0) atomicExch(p.words + 1, 1);
 }
-// part 2 or 3
-__device__ __forceinline__ void enter_groups(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c, int part,
-                                             float* A, float* H) {
+// Part 2: the state that leaves the group before (0: there is none).  Every eighth
+// group from the last one back is looked at, without a wait; from the latest one in
+// which every channel of the wave has a state (or the first) on, the groups are waited for and
+// applied.  Up to 16 groups two batches of loads read them all, and the look would be a third.
+__device__ __forceinline__ float enter_groups(const LinrecLaunch& p, int64_t tile, int j, int dir, int64_t c) {
     // a group's row is a sixteenth of its last tile's, which no other group's is
-    const int64_t first = (tile + (int64_t)dir * (GROUP - 1 - j)) / GROUP;
-    const int ng = j / GROUP, half = (ng + 1) / 2, s0 = (part - 2) * half, n = min(ng - s0, half);
+    const int64_t first = (tile + (int64_t)dir * (GROUP - 1 - j)) / GROUP, step = (int64_t)dir * p.D;
+    const uint64_t* row = p.groups + first * p.D;
+    const int ng = j / GROUP;
+    int s = 0;
+    for (int last = ng - 1; s == 0 && last >= 16; last -= BATCH * BATCH) {
+        unsigned v[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) v[k] = (unsigned)peek(row + max(last - k * BATCH, 0) * step, (unsigned)c * 8);
+#pragma unroll
+        for (int k = BATCH - 1; k >= 0; --k)
+            if (__ballot(v[k] != STATE) == 0) s = max(last - k * BATCH, 0);
+    }
     int polls = POLLS;
-    *A = 1.f;
-    *H = 0.f;
-    compose(p.groups + (first + (int64_t)dir * s0) * p.D, (int64_t)dir * p.D, n, c, A, H, &polls, p.words + 1);
-    if (part == 2 && ng > 0) *A = 0.f;
+    float A = 1.f, H = 0.f;
+    compose(row + s * step, step, ng - s, c, &A, &H, &polls, p.words + 1);
     if (polls <= 0) atomicExch(p.words + 1, 1);
+    return H;
 }
 // the tile's own pair; and once the parts of its group are there, the group's
 __device__ __forceinline__ void publish_tile(const LinrecLaunch& p, int64_t tile, int j, int nt, int64_t c, float A,
                                              float H, float start) {
-    if (j + 1 < nt) publish(p.pairs + tile * p.D + c, j == 0 ? 0.f : A, j == 0 ? A * start + H : H);
+    if (j + 1 >= nt) return;
+    if (j == 0) publish_state(p.pairs + tile * p.D + c, A * start + H);
+    else publish(p.pairs + tile * p.D + c, A, H);
 }
 // (only of a group that has tiles behind it: closes_group)
 __device__ __forceinline__ bool closes_group(int j, int nt) { return j % GROUP == GROUP - 1 && j + 1 < nt; }
-template <int CB>
+// LEFT: once the state that enters the group is there too, the state that leaves it, by the
+// operations that a tile which reads the pair applies to that state.
+template <bool LEFT, int CB>
 __device__ __forceinline__ void publish_group(const LinrecLaunch& p, int64_t tile, int j, int64_t c, float A, float H,
                                               const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
-    publish(p.groups + (tile / GROUP) * p.D + c, j < GROUP ? 0.f : s_pA[0][k] * s_pA[1][k] * A,
-            A * (s_pA[1][k] * s_pH[0][k] + s_pH[1][k]) + H);
+    uint64_t* to = p.groups + (tile / GROUP) * p.D + c;
+    const float gA = s_pA[0][k] * s_pA[1][k] * A;
+    const float gH = __builtin_fmaf(A, __builtin_fmaf(s_pA[1][k], s_pH[0][k], s_pH[1][k]), H);
+    if (LEFT) publish_state(to, __builtin_fmaf(gA, s_pH[2][k], gH));
+    else if (j < GROUP) publish_state(to, gH);
+    else publish(to, gA, gH);
 }
 template <int CB> __device__ __forceinline__ float entering(const float (*s_pA)[CB], const float (*s_pH)[CB], int k) {
-    float v = s_pH[2][k];
-    v = s_pA[3][k] * v + s_pH[3][k];
-    v = s_pA[0][k] * v + s_pH[0][k];
+    const float v = s_pA[0][k] * s_pH[2][k] + s_pH[0][k];
     return s_pA[1][k] * v + s_pH[1][k];
 }
 
@@ -386,11 +412,12 @@ __device__ __forceinline__ void fwd_tile(const LinrecLaunch& p, const Tile& t, i
         }
         if (closes) {        // before waiting for other groups, or the groups would wait in a row
             __syncthreads();
-            if (own) publish_group<CB>(p, tile, t.j, c0 + k, tA, tH, s_pA, s_pH, k);
+            if (own) publish_group<false, CB>(p, tile, t.j, c0 + k, tA, tH, s_pA, s_pH, k);
         }
-        if (live && part >= 2) enter_groups(p, tile, t.j, 1, c0 + k, part, &s_pA[part][k], &s_pH[part][k]);
+        if (live && part == 2) s_pH[2][k] = enter_groups(p, tile, t.j, 1, c0 + k);
         __syncthreads();
         if (own) {
+            if (closes && t.j >= GROUP) publish_group<true, CB>(p, tile, t.j, c0 + k, tA, tH, s_pA, s_pH, k);
             const float in = entering<CB>(s_pA, s_pH, k);
             if (p.states) p.states[tile * p.D + c0 + k] = in;
             if (p.ht && t.j + 1 == t.nt) p.ht[t.seq * p.D + c0 + k] = tA * in + tH;
@@ -422,7 +449,7 @@ template <int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, i
 __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
     static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
-    __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[HAND ? NT : 1][CB], s_pH[HAND ? NT : 1][CB];
+    __shared__ float s_A[NW][CB], s_H[NW][CB], s_pA[HAND ? 2 : 1][CB], s_pH[HAND ? NT : 1][CB];
     __shared__ unsigned s_ticket;
     unsigned tile, block;
     while (tile_by_ticket<HAND>(p, (unsigned)((p.D + CB - 1) / CB), false, &tile, &block, &s_ticket)) {
@@ -534,11 +561,12 @@ __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, i
         }
         if (closes) {        // before waiting for other groups, or the groups would wait in a row
             __syncthreads();
-            if (own) publish_group<CB>(p, tile, back, c0 + k, tA, tE, s_pA, s_pE, k);
+            if (own) publish_group<false, CB>(p, tile, back, c0 + k, tA, tE, s_pA, s_pE, k);
         }
-        if (live && part >= 2) enter_groups(p, tile, back, -1, c0 + k, part, &s_pA[part][k], &s_pE[part][k]);
+        if (live && part == 2) s_pE[2][k] = enter_groups(p, tile, back, -1, c0 + k);
         __syncthreads();
         if (own) {
+            if (closes && back >= GROUP) publish_group<true, CB>(p, tile, back, c0 + k, tA, tE, s_pA, s_pE, k);
             if (p.dh0 && t.j == 0) p.dh0[t.seq * p.D + c0 + k] = tA * entering<CB>(s_pA, s_pE, k) + tE;
         }
 #pragma unroll
@@ -626,7 +654,7 @@ __global__ __launch_bounds__(64 * NW) void linrec_bwd_kernel(LinrecLaunch p) {
     constexpr int CB = 64 * V;
     static_assert(!HAND || NT * CB <= 64 * NW, "NT threads to a channel of the block");
     __shared__ float s_A[NW][CB], s_H[NW][CB], s_E[NW][CB];
-    __shared__ float s_pA[HAND ? NT : 1][CB], s_pE[HAND ? NT : 1][CB], s_in[CB];
+    __shared__ float s_pA[HAND ? 2 : 1][CB], s_pE[HAND ? NT : 1][CB], s_in[CB];
     // log2 a and sigmoid of every token, each thread's own: they are wanted again only at
     // the end, and next to a, m, x and dy there are no registers for them
     __shared__ f32x2v s_gate[ACT ? S * V : 1][64 * NW];

@@ -419,3 +419,45 @@ def test_offsets_check(gpu_lib):
             with pytest.raises(gdn.GdnError) as e:
                 f()
             assert e.value.status == 8
+
+
+@pytest.mark.parametrize("first", [0, 100])
+def test_growing_gates(gpu_lib, first):
+    """Gates above 0 whose products are finite over 2048 tokens (4e3) but not over the sequence: zero states
+    stay zero, and states that start late, or gradients that start early, are the definition's."""
+    T, D = 65536, 5
+    print("case: linrec growing", first, flush=True)
+    r = torch.Generator().manual_seed(91)
+    g = torch.tensor([0.004, 0.004, 0.003, 0.0008, -0.01]).repeat(1, first + T, 1)
+    x, dy = (torch.rand(1, first + T, D, generator=r) + 0.5 for _ in range(2))
+    late, early = first + 52000, first + 13000
+    x[:, :, 0] = 0.0
+    dy[:, :, 0] = 0.0
+    x[:, :late, 1:3] = 0.0
+    dy[:, early:, 1:3] = 0.0
+    cu = torch.tensor([0, first, first + T]) if first else None
+    x, g, dy = x.cuda(), g.cuda(), dy.cuda()
+    dev = None if cu is None else cu.cuda()
+    states = gpu_lib.linrec_states(x, dev)
+    y, ht = gpu_lib.linrec_fwd(x, g, cu_seqlens=dev, states=states)
+    got = gpu_lib.linrec_bwd(x, g, dy, cu_seqlens=dev, states=states)
+    torch.cuda.synchronize()
+    want, err = ref.linrec(x, g, cu=cu, dy=dy)
+    ref.check_all(dict(got, y=y, ht=ht), want, err)
+
+
+def test_same_bits_of_a_long_sequence(gpu_lib):
+    """Where a tile starts among the groups before it depends on timing; the bits do not."""
+    T, D = 100000, 130
+    print("case: linrec long bits", T, D, flush=True)
+    r = torch.Generator().manual_seed(94)
+    x, dy = (torch.randn(1, T, D, generator=r).cuda() for _ in range(2))
+    g = (-torch.rand(1, T, D, generator=r) * 1e-3).cuda()
+
+    def call():
+        y, ht = gpu_lib.linrec_fwd(x, g)
+        return dict(gpu_lib.linrec_bwd(x, g, dy), y=y, ht=ht)
+    first = call()
+    for _ in range(5):
+        again = call()
+        assert all(torch.equal(first[n], again[n]) for n in first)
