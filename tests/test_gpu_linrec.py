@@ -446,6 +446,75 @@ def test_growing_gates(gpu_lib, first):
     ref.check_all(dict(got, y=y, ht=ht), want, err)
 
 
+def whole_numbers(seed, lengths, D, resets):
+    """x, g, h0, dy, dht whose recurrence is exact in 32 bits (gates of 0, some of minus infinity, whole numbers),
+    and its results: sums between resets."""
+    r = torch.Generator().manual_seed(seed)
+    T, N = sum(lengths), len(lengths)
+    x, dy = (torch.randint(1, 100, (T, D), generator=r) for _ in range(2))
+    h0, dht = (torch.randint(-99, 100, (N, D), generator=r) for _ in range(2))
+    cut = torch.rand(T, D, generator=r) < resets
+    want = dict(y=torch.zeros(T, D), dx=torch.zeros(T, D), dg=torch.zeros(T, D), ht=h0.double(), dh0=dht.double())
+    want = {k: v.double() for k, v in want.items()}
+    at = 0
+    for n, length in enumerate(lengths):
+        if length == 0:
+            continue
+        s = slice(at, at + length)
+        at += length
+        i = torch.arange(length)[:, None]
+
+        def sums(v, first, reset):      # of v since the last reset, `first` in front
+            c = v.cumsum(0)
+            last = torch.where(reset, i, -1).cummax(0).values
+            base = torch.where(last > 0, c.gather(0, (last - 1).clamp(min=0)), torch.zeros_like(c))
+            return c - base + torch.where(last < 0, first, torch.zeros_like(first))
+        h = sums(x[s], h0[n], cut[s])
+        # dh_t = dy_t + a_{t+1} dh_{t+1}: from the end, a reset at t + 1 comes before token t
+        back = torch.cat([torch.zeros(1, D, dtype=torch.bool), cut[s].flip(0)[:-1]])
+        dh = sums(dy[s].flip(0), dht[n], back).flip(0)
+        a = (~cut[s]).long()
+        before = torch.cat([h0[n][None], h[:-1]])
+        want["y"][s], want["dx"][s], want["dg"][s] = h.double(), dh.double(), (a * dh * before).double()
+        want["ht"][n], want["dh0"][n] = h[-1].double(), (a * dh)[0].double()
+    assert all(want[k].abs().max() < 2 ** 24 for k in ("y", "dx", "ht", "dh0")) and want["dg"].abs().max() < 2 ** 53
+    g = torch.where(cut, float("-inf"), 0.0)
+    return dict(x=x.float()[None], dy=dy.float()[None], g=g[None], h0=h0.float(), dht=dht.float()), want
+
+
+@pytest.mark.parametrize("lengths", [(40037,), (70001, 0, 128 * 16 * 9, 128 * 16 * 9 + 1), (2,) * 4000 + (45000, 3, 0, 20000),
+                                     (150000,)])
+@pytest.mark.parametrize("D", [3, 6])
+@pytest.mark.parametrize("resets", [0.0, 1e-4])
+def test_many_groups_exactly(gpu_lib, lengths, D, resets):
+    """Sequences of many groups of tiles, packed ones among short ones too: every pair once and in order."""
+    print("case: linrec groups", len(lengths), sum(lengths), D, resets, flush=True)
+    d, want = whole_numbers(92, lengths, D, resets)
+    d = {k: v.cuda() for k, v in d.items()}
+    cu = torch.tensor([0] + list(lengths)).cumsum(0).cuda() if len(lengths) > 1 else None
+    for keep in (False, True):
+        states = gpu_lib.linrec_states(d["x"], cu) if keep else None
+        y, ht = gpu_lib.linrec_fwd(d["x"], d["g"], h0=d["h0"], cu_seqlens=cu, states=states)
+        got = gpu_lib.linrec_bwd(d["x"], d["g"], d["dy"], h0=d["h0"], dht=d["dht"], cu_seqlens=cu, states=states)
+        torch.cuda.synchronize()
+        got.update(y=y, ht=ht)
+        for k, w in want.items():
+            assert torch.equal(got[k].cpu().view(w.shape), w.float()), (k, keep)
+
+
+@pytest.mark.parametrize("lengths", [(40037,), (2,) * 3500 + (40000, 5)])
+def test_many_groups_of_slow_gates(gpu_lib, lengths):
+    """Decays slow enough for far groups to count, inputs above 0 so that none is lost in the bound."""
+    T, N, D = sum(lengths), len(lengths), 6
+    print("case: linrec slow", N, T, flush=True)
+    r = torch.Generator().manual_seed(93)
+    g = -torch.rand(1, T, D, generator=r) * torch.tensor([2e-5, 2e-4, 2e-3, 2e-4, 2e-5, 2e-2])
+    x, dy = (torch.rand(1, T, D, generator=r).cuda() + 0.5 for _ in range(2))
+    h0, dht = (torch.rand(N, D, generator=r).cuda() for _ in range(2))
+    cu = torch.tensor([0] + list(lengths)).cumsum(0) if N > 1 else None
+    both(gpu_lib, dict(x=x, g=g.cuda(), dy=dy, h0=h0, dht=dht, A_log=None, dt_bias=None), cu, normalize=True)
+
+
 def test_same_bits_of_a_long_sequence(gpu_lib):
     """Where a tile starts among the groups before it depends on timing; the bits do not."""
     T, D = 100000, 130
