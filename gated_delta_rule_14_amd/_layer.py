@@ -210,12 +210,14 @@ def _linrec(x, g, normalize, A_log, dt_bias, y, dims):
     return dev, sh, act, key
 
 
-def linrec_states(x, cu_seqlens=None):
-    """A buffer for linrec_fwd's `states` (of x [B, T, D]), to be kept for linrec_bwd."""
+def linrec_states(x, cu_seqlens=None, stream=None):
+    """A buffer for linrec_fwd's `states` (of x [B, T, D]), to be kept for
+    linrec_bwd; `stream`: the one these calls are given."""
     dev = _device(x, "x")
     B, T, D = x.shape
     p = _linrec_plan(B, T, D, _cu(cu_seqlens, dev), 0, 0, 0, 0, 0, 0)
-    return x.new_empty((p.rows, D), dtype=_F32)
+    with _on(stream):   # allocated on the kernels' stream (see chunk_fwd)
+        return x.new_empty((p.rows, D), dtype=_F32)
 
 
 def linrec_fwd(x, g, h0=None, cu_seqlens=None, normalize=False, A_log=None, dt_bias=None,

@@ -530,3 +530,28 @@ def test_same_bits_of_a_long_sequence(gpu_lib):
     for _ in range(5):
         again = call()
         assert all(torch.equal(first[n], again[n]) for n in first)
+
+
+def test_states_belong_to_their_stream(gpu_lib):
+    """The buffer of the tiles' states comes from the memory of the stream whose kernels use it, and goes back there."""
+    s = torch.cuda.Stream()
+    x = torch.zeros(1, 8192, 4096, dtype=BF, device="cuda")
+    print("case: linrec states on a stream", flush=True)
+    for stream, other in ((s, torch.cuda.current_stream()), (None, s)):
+        own = torch.cuda.current_stream() if stream is None else stream
+        keep = gpu_lib.linrec_states(x, stream=stream)
+        shape, at = keep.shape, keep.data_ptr()
+        del keep
+        with torch.cuda.stream(other):
+            there = torch.empty(shape, device="cuda")
+        with torch.cuda.stream(own):
+            here = torch.empty(shape, device="cuda")
+        assert here.data_ptr() == at and there.data_ptr() != at
+        del here, there     # or the next pass finds a block that it frees itself
+    x, g = x + 1, x.float() - 0.5
+    want, _ = gpu_lib.linrec_fwd(x, g)
+    torch.cuda.synchronize()
+    keep = gpu_lib.linrec_states(x, stream=s)
+    got, _ = gpu_lib.linrec_fwd(x, g, states=keep, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
