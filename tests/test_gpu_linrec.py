@@ -555,3 +555,17 @@ def test_states_belong_to_their_stream(gpu_lib):
     got, _ = gpu_lib.linrec_fwd(x, g, states=keep, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("T", [1, 16, 64, 200, 2500])
+def test_gradients_at_gate_extremes(gpu_lib, normalize, T):
+    """Gates of 0, minus infinity and just below 0: the gradients are the definition's, the slope of
+    sqrt(1 - a^2) being taken as 0 where a = 1."""
+    print("case: linrec gate extremes", T, normalize, flush=True)
+    d = inputs(95, 1, T, 10, F32, F32)
+    d["g"][:, ::3] = 0.0
+    d["g"][:, 1::7] = float("-inf")
+    d["g"][:, 2::11] = -1e-30
+    both(gpu_lib, d, normalize=normalize)
+    both(gpu_lib, d, normalize=normalize, h0=False, dht=False, keep=False)
