@@ -153,7 +153,7 @@ def _words(ws, dev, stream, packed, waits=False):
     if ws is None or not (packed or waits) or not _debug():
         return
     (stream or torch.cuda.current_stream(dev)).synchronize()
-    bad, wait = ws.view(torch.uint8)[:8].view(torch.int32).cpu().tolist()
+    bad, wait = ws.view(-1).view(torch.uint8)[:8].view(torch.int32).cpu().tolist()
     if packed and bad:
         raise GdnError(8, "cu_seqlens must start at 0, never decrease and end at T")
     if waits and wait:

@@ -569,3 +569,20 @@ def test_gradients_at_gate_extremes(gpu_lib, normalize, T):
     d["g"][:, 2::11] = -1e-30
     both(gpu_lib, d, normalize=normalize)
     both(gpu_lib, d, normalize=normalize, h0=False, dht=False, keep=False)
+
+
+@pytest.mark.parametrize("shape", [(1, 1 << 20), (1 << 10, 1 << 10), (64, 64, 64)])
+def test_workspace_of_any_shape_and_type(gpu_lib, shape):
+    """A supplied workspace counts by its bytes, also where the status words are read from it."""
+    print("case: linrec workspace", shape, flush=True)
+    d = inputs(96, 1, 300, 24, N=2)
+    cu = torch.tensor([0, 100, 300], device="cuda")
+    want = gpu_lib.linrec_fwd(d["x"], d["g"], cu_seqlens=cu)
+    for dt in (torch.uint8, F32):
+        ws = torch.zeros(shape, dtype=dt, device="cuda")
+        got = gpu_lib.linrec_fwd(d["x"], d["g"], cu_seqlens=cu, workspace=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        with pytest.raises(gpu_lib.GdnError) as e:
+            gpu_lib.linrec_fwd(d["x"], d["g"], cu_seqlens=cu + 1, workspace=ws)
+        assert e.value.status == 8
