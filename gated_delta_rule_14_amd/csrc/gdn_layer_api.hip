@@ -150,9 +150,9 @@ LinrecLayout linrec_layout(const gdn_linrec_desc* d, bool backward) {
     const int64_t D = d->channels;
     // Sequences of up to 16 tokens run by a wave or two instead of a tile's workgroup of 8 or
     // 16, of up to 64 by half of it (256 sequences of 4 tokens, 4096 channels: forward 124 ->
-    // 11 us, backward 339 -> 31). Of packed input only the mean length is known here: short
+    // 10 us, backward 339 -> 29). Of packed input only the mean length is known here: short
     // ones are looked for where it is below half a tile (2500 sequences of 3 tokens: 1267 ->
-    // 88 and 3507 -> 222 us).
+    // 88 and 3507 -> 222 us; lengths that differ much are not measured).
     const bool packed = d->num_seqs > 0;
     const int64_t T = d->seq_len, mean = packed ? T / d->num_seqs : T;
     const int few = mean > 64 - packed ? 0 : mean > 16 - packed ? 64 : 16;

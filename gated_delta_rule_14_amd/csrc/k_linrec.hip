@@ -33,7 +33,7 @@
 //
 // Measured (bf16 x and y): 4 x 4096 tokens of 2048 channels with fp32 gates 58 us,
 // 4.6 TB/s; 137 thousand packed tokens of 4096 channels with raw gates and
-// normalised inputs 0.70 ms, bound by the vector ALU (32 instructions and 3
+// normalised inputs 0.69 ms, bound by the vector ALU (32 instructions and 3
 // transcendentals a token and channel, 0.63 ms of issue slots).  A tile is 128
 // tokens and 128 channels, 16 tokens to a wave: tiles of 64 tokens take 15 to
 // 35 % longer (a hand-off for half the work), of 256 leave one workgroup to a
@@ -470,8 +470,8 @@ __global__ __launch_bounds__(64 * NW, 4) void linrec_fwd_kernel(LinrecLaunch p) 
 // tile, kept by the forward.  16 waves of 8 tokens: a, m, x, dy and the states
 // of 16 values a thread are what 128 registers hold.  2 x 8192 tokens of 2048
 // channels, bf16, raw gates, normalised: 116 us against 66 us of bytes and 73
-// us of ALU slots; one workgroup fills a CU, so the loads and the hand-off of
-// a tile are not hidden by another.
+// us of ALU slots; one workgroup fills a CU (159 KB of LDS, 16 waves of 128 registers), so
+// the loads and the hand-off of a tile are not hidden by another.
 template <bool FULL, int HAND, typename X, typename G, bool ACT, bool NORM, int V, int S, int NW>
 __device__ __forceinline__ void bwd_tile(const LinrecLaunch& p, const Tile& t, int64_t tile, int64_t c0,
                                          float (*s_A)[64 * V], float (*s_H)[64 * V], float (*s_E)[64 * V],

@@ -8,10 +8,10 @@
 // token, so the angle's 64-bit arithmetic is paid once for q_heads + k_heads
 // rows.  Few tokens (decode) split their heads over several waves.
 //
-// Measured (bf16): 4 x 4096 tokens of 16 + 16 heads of 128, 45 us, 6.0 TB/s
+// Measured (bf16): 4 x 4096 tokens of 16 + 16 heads of 128, 51 us, 5.3 TB/s
 // with part of it in the cache; 16411 tokens of 32 + 8 heads, 67 us forward
-// (5.0 TB/s, a large copy's rate) and 115 us backward (4.4 TB/s); 64 tokens of
-// 16 + 2 heads of 256, 4.8 us.
+// (5.0 TB/s, a large copy's rate) and 122 us backward with the sums for the weights (4.1
+// TB/s); 64 tokens of 16 + 2 heads of 256, 5.0 us.
 //
 // The element that a half-split rotation pairs with sits R/16 lanes away and
 // comes by a lane shuffle; interleaved pairs are in the lane itself.
