@@ -13,7 +13,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
-ABI_VERSION = 10
+ABI_VERSION = 11
 
 DTYPE_F32, DTYPE_BF16 = 0, 1
 GATE_SCALAR, GATE_PER_KEY = 0, 1
@@ -31,7 +31,10 @@ EXPORTS = sorted(["gdn_abi_version", "gdn_status_str", "gdn_last_error",
                   "gdn_linrec_workspace", "gdn_linrec_fwd", "gdn_linrec_bwd", "gdn_linrec_step",
                   "gdn_qk_norm_rope", "gdn_qk_norm_rope_bwd_workspace", "gdn_qk_norm_rope_bwd",
                   "gdn_short_conv_workspace", "gdn_short_conv_fwd", "gdn_short_conv_bwd",
-                  "gdn_short_conv_step"])
+                  "gdn_short_conv_step",
+                  "gdn_decay_attn_workspace", "gdn_decay_attn_fwd", "gdn_decay_attn_bwd",
+                  "gdn_decay_attn_step",
+                  "gdn_paged_append", "gdn_paged_attn_workspace", "gdn_paged_attn"])
 INTRA_STORE_AINV = 1
 ACT_GATE, ACT_BETA_SIGMOID, ACT_BETA_NEG_EIG, ACT_QK_L2NORM = 1, 2, 4, 8
 
@@ -127,8 +130,9 @@ def load(path: str = LIB_PATH):
     v = lib.gdn_abi_version()
     if v != ABI_VERSION:
         raise RuntimeError("libgdn.so ABI %d, binding expects %d" % (v, ABI_VERSION))
-    from . import _layer
+    from . import _layer, _mixer
     _layer.declare(lib)
+    _mixer.declare(lib)
     _lib = lib
     return lib
 

@@ -1,0 +1,176 @@
+// Linear attention with a decay for each head: the walks of segments alone, the
+// chaining of their states, the gates' gradient and the single-token step.  The
+// chunk walk itself, its mathematics and its figures are in k_decay.hpp.
+#include "k_decay.hpp"
+
+namespace gdn {
+
+hipError_t launch_walk_local(const DecayWalk& p, int K, int V, bool bf, bool rev) {
+    return rev ? launch_walk_of<true, false, 0, true>(p, K, V, bf) : launch_walk_of<false, false, 0, true>(p, K, V, bf);
+}
+
+hipError_t launch_decay_walk(const DecayWalk& p, DecayKind kind, int K, int V, bool bf) {
+    switch (kind) {
+        case DECAY_O: return launch_walk_o(p, K, V, bf);
+        case DECAY_DQ: return launch_walk_dq(p, K, V, bf);
+        case DECAY_DK: return launch_walk_dk(p, K, V, bf);
+        case DECAY_DV: return launch_walk_dv(p, K, V, bf);
+        case DECAY_LOCAL: return launch_walk_local(p, K, V, bf, false);
+        case DECAY_LOCAL_REV: return launch_walk_local(p, K, V, bf, true);
+    }
+    return hipErrorInvalidValue;
+}
+
+// S_0 = first, S_{j+1} = dec_j S_j + local_j over a sequence's segments; S_j takes
+// the place of local_j.  A workgroup takes 1024 elements of a sequence's state, by
+// the block of its first segment.
+__global__ __launch_bounds__(256) void decay_join_kernel(DecayJoin a) {
+    const int64_t per = (a.KV + 1023) / 1024, hb = a.H * per;
+    const int64_t c = blockIdx.x / hb, rest = blockIdx.x - c * hb, h = rest / per;
+    const int64_t e = (rest - h * per) * 1024 + threadIdx.x * 4;
+    const Tile t = tile_of(a.map, c);
+    if (t.n == 0 || t.j != 0 || e >= a.KV) return;
+    f32x4 s = zero4();
+    if (a.first) s = *reinterpret_cast<const f32x4*>(a.first + (t.seq * a.H + h) * a.KV + e);
+    const int64_t step = a.rev ? -1 : 1;
+    int64_t at = c + (a.rev ? t.nt - 1 : 0);
+    f32x4 next = *reinterpret_cast<const f32x4*>(a.state + (at * a.H + h) * a.KV + e);
+    for (int j = 0; j < t.nt; ++j, at += step) {
+        f32x4* p = reinterpret_cast<f32x4*>(a.state + (at * a.H + h) * a.KV + e);
+        const f32x4 own = next;
+        if (j + 1 < t.nt) next = *reinterpret_cast<const f32x4*>(a.state + ((at + step) * a.H + h) * a.KV + e);
+        *p = s;
+        if (j + 1 < t.nt) {            // (the last one walked has no local state)
+            const float d = a.dec[at * a.H + h];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = fmaf(d, s[i], own[i]);
+        }
+    }
+}
+
+hipError_t launch_decay_join(const DecayJoin& a) {
+    const int64_t blocks = a.tiles * a.H * ((a.KV + 1023) / 1024);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)blocks), dim3(256), 0, a.stream, a);
+    return hipGetLastError();
+}
+
+// dg_t = <S, E> at the segment's end + the sum of the dots from t on, in 64 bits;
+// 0 where the gate lets nothing through.  A wave takes a segment of a head, 64
+// tokens at a time from its end.
+__global__ __launch_bounds__(64) void decay_gate_kernel(DecayGate a) {
+    const int lane = threadIdx.x;
+    const int64_t blk = blockIdx.x / a.H, h = blockIdx.x - blk * a.H;
+    int64_t row0;
+    int n;
+    if (blk < a.tiles) {
+        const Tile t = tile_of(a.map, blk);
+        row0 = t.row0;
+        n = t.n;
+    } else if (a.map.seqs) {
+        const int4 q = a.map.seqs[blk - a.tiles];
+        row0 = q.x;
+        n = q.y > a.map.tile ? 0 : q.y;
+    } else {
+        row0 = (blk - a.tiles) * a.map.T;
+        n = (int)a.map.T;
+    }
+    if (n == 0) return;
+    double carry = a.ends[blk * a.H + h];
+    const float *dq = a.dq + h * a.tokens + row0, *dk = a.dk + h * a.tokens + row0;
+    for (int t0 = (n - 1) & ~63; t0 >= 0; t0 -= 64) {
+        const int t = t0 + 63 - lane;     // lane 0 takes the last token
+        double x = t < n ? (double)dq[t] - (double)dk[t] : 0.0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double y = __shfl_up(x, off, 64);
+            if (lane >= off) x += y;
+        }
+        x += carry;
+        if (t < n) {
+            const float g = a.g[(row0 + t) * a.gs + h];
+            a.dg[(row0 + t) * a.H + h] = gate_parts(g).hi == -8192.f ? 0.f : (float)x;
+        }
+        carry = __shfl(x, 63, 64);
+    }
+}
+
+hipError_t launch_decay_gate(const DecayGate& a) {
+    const int64_t blocks = (a.tiles + a.singles) * a.H;
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(decay_gate_kernel, dim3((unsigned)blocks), dim3(64), 0, a.stream, a);
+    return hipGetLastError();
+}
+
+// One token: S <- e^g S + k v^T, o = scale q S, the state read and written once.
+// A workgroup takes VS columns of a state; thread t the four columns t % (VS / 4)
+// of its rows.
+template <typename T, int K, int V, int VS>
+__global__ __launch_bounds__(256) void decay_step_kernel(DecayStep a) {
+    constexpr int CG = VS / 4, RG = 256 / CG, ROWS = K / RG, NS = V / VS;
+    static_assert(CG * RG == 256 && ROWS * RG == K, "shape");
+    __shared__ float s_q[K], s_k[K];
+    __shared__ f32x4 s_o[RG][CG];
+    const int64_t pair = blockIdx.x / NS;
+    const int slice = (int)(blockIdx.x - pair * NS), tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
+    const int64_t n = pair / a.H, h = pair - n * a.H;
+    const int col = slice * VS + 4 * cg;
+    float* st = a.state + pair * (K * V) + (int64_t)rg * ROWS * V + col;
+    f32x4 s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) s[i] = *reinterpret_cast<const f32x4*>(st + i * V);
+    const T* q = static_cast<const T*>(a.q.p) + n * a.q.ts + (h / a.q.div) * a.q.hs;
+    const T* k = static_cast<const T*>(a.k.p) + n * a.k.ts + (h / a.k.div) * a.k.hs;
+    const T* v = static_cast<const T*>(a.v.p) + n * a.v.ts + h * a.v.hs + col;
+    const f32x4 vv = Quad<T>::get(Quad<T>::load(v));
+    const float d = expf(a.g[n * a.gs + h]);
+    if (tid < K) {
+        s_q[tid] = Elem<T>::load(q + tid);
+        s_k[tid] = Elem<T>::load(k + tid);
+    }
+    __syncthreads();
+    f32x4 o = zero4();
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const float kr = s_k[rg * ROWS + i], qr = s_q[rg * ROWS + i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[i][e] = fmaf(d, s[i][e], kr * vv[e]);
+            o[e] = fmaf(qr, s[i][e], o[e]);
+        }
+        __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(st + i * V));
+    }
+    s_o[rg][cg] = o;
+    __syncthreads();
+    if (rg != 0) return;
+    for (int i = 1; i < RG; ++i) {
+        const f32x4 x = s_o[i][cg];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= a.scale;
+    store4(static_cast<T*>(a.o) + pair * V + col, o);
+}
+
+template <typename T, int K, int V>
+static hipError_t step_of(const DecayStep& a) {
+    // a state is cut into slices of 32 columns where whole states would not fill the chip twice
+    const int64_t pairs = a.N * a.H;
+    if (pairs < 512)
+        hipLaunchKernelGGL((decay_step_kernel<T, K, V, 32>), dim3((unsigned)(pairs * (V / 32))), dim3(256), 0, a.stream, a);
+    else
+        hipLaunchKernelGGL((decay_step_kernel<T, K, V, V>), dim3((unsigned)pairs), dim3(256), 0, a.stream, a);
+    return hipGetLastError();
+}
+template <typename T>
+static hipError_t step_dt(const DecayStep& a) {
+    if (a.K == 64) return a.V == 64 ? step_of<T, 64, 64>(a) : step_of<T, 64, 128>(a);
+    return a.V == 64 ? step_of<T, 128, 64>(a) : step_of<T, 128, 128>(a);
+}
+hipError_t launch_decay_step(const DecayStep& a) {
+    if (a.N * a.H == 0) return hipSuccess;
+    return a.bf16 ? step_dt<bf16>(a) : step_dt<float>(a);
+}
+
+}  // namespace gdn

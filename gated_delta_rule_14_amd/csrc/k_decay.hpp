@@ -1,0 +1,488 @@
+// Linear attention with a decay for each head, in chunks of 64 tokens.
+//
+// Forward, per state head, with G_i = g_first + ... + g_i inside a chunk and
+// S the state entering it:
+//   o_i = scale (e^{G_i} q_i S + sum_{j<=i} e^{G_i-G_j} (q_i k_j) v_j)
+//   S'  = e^{G_last} S + sum_j e^{G_last-G_j} k_j v_j^T
+// Its gradients are the same walk over other operands: with E the gradient of
+// the state behind a chunk,
+//   dq_i = scale (e^{G_i} do_i S^T + sum_{j<=i} e^{G_i-G_j} (do_i v_j) k_j)
+//   dk_j = e^{G_last-G_j} v_j E^T + scale sum_{i>=j} e^{G_i-G_j} (v_j do_i) q_i
+//   dv_j = e^{G_last-G_j} k_j E + scale sum_{i>=j} e^{G_i-G_j} (k_j q_i) do_i
+//   E'   = e^{G_last} E + scale sum_i e^{G_i} q_i do_i^T
+// so one kernel does all of them: out = a S + (a b^T) c, S += b c^T, with
+// (a, b, c) = (q, k, v), (do, v, k), (v, do, q) and (k, q, do), the last two
+// from the last chunk to the first.  dg_t sums every pair i >= t > j, the
+// states before and the gradients behind; per chunk
+//   dg_t = <S', E> + sum_{i>=t} (qs_i + R_i - C_i - ks_i),
+// qs_i = q_i times the state's part of dq_i, ks_i = k_i times that of dk_i,
+// R and C the row and column sums of the pairs (q_i k_j)(do_i v_j) e^{G_i-G_j},
+// j < i: sums of decayed terms only, so strong decays keep their digits.
+//
+// A workgroup of four waves walks the chunks of one segment of one head.  The
+// waves own a quarter of the columns of c and S each; S stays in MFMA
+// accumulators, whose layout is that of an operand over its own rows, so S
+// never passes through LDS.  The pairs' products of the chunk are made once,
+// a tile row to a wave, and handed round in LDS.  Long sequences are cut into
+// segments: a first walk makes each segment's own state, launch_decay_join
+// chains them, and the segments then run side by side.
+//
+// Roundings: products are of the inputs' type, sums in 32 bits.  With bf16 the
+// pairs' weights and the state are rounded to bf16 where they are multiplied
+// into an output of that type (each as much as the output's own rounding); where
+// a 32-bit result depends on them (the state itself, dg) the factor is split into
+// three bf16 parts, 24 bits, and multiplied part by part.
+#pragma once
+
+#include "gdn_mixer.hpp"
+#include "gdn_mma8.hpp"
+
+namespace gdn {
+
+// A chunk's rows on their way from memory to LDS: PER 16-byte units to a thread.
+template <typename T, int D> struct Ahead {
+    typedef Rows<T, D> R;
+    u32x4 u[R::PER];
+    __device__ __forceinline__ void load(const T* base, int64_t ts, int n, int tid) {
+#pragma unroll
+        for (int i = 0; i < R::PER; ++i) {
+            const int q = tid + 256 * i, row = q / R::UR, unit = q % R::UR;
+            u[i] = u32x4{0, 0, 0, 0};
+            if (row < n) u[i] = *reinterpret_cast<const u32x4*>(base + row * ts + unit * R::U);
+        }
+    }
+    __device__ __forceinline__ void put(const R& r, int tid) const {
+#pragma unroll
+        for (int i = 0; i < R::PER; ++i) {
+            const int q = tid + 256 * i;
+            *reinterpret_cast<u32x4*>(r.p + R::at(q / R::UR, q % R::UR)) = u[i];
+        }
+    }
+};
+
+// Gates of a chunk in log2, as a multiple of 1/16 and a rest of up to 1/32, whose
+// running sums are exact and below 2 (the sum of the gates themselves would lose
+// the small ones behind a large one).  A gate below -150 (2^-150 is 0 in 32 bits)
+// counts as -8192, whose power and every sum with it is 0: nothing passes it.
+struct GateParts {
+    float hi, lo;
+};
+__device__ __forceinline__ GateParts gate_parts(float g) {
+    const float x = g * LOG2E;
+    if (x < -150.f) return {-8192.f, 0.f};
+    if (x > 8192.f) return {8192.f, 0.f};
+    const float h = rintf(x * 16.f) * 0.0625f;
+    return {h, fmaf(g, LOG2E, -h)};   // NaN stays one
+}
+
+// What the waves need of a chunk's gates: sums up to each token (reversed walks:
+// from behind it), the factors of the state in and out, and of the whole chunk.
+struct alignas(16) ChunkGates {
+    float hi[64], lo[64], in[64], out[64];
+    float dec;
+};
+template <bool REV>
+__device__ __forceinline__ void make_gates(ChunkGates& s, float g, float in_scale, float up_scale, int lane) {
+    const GateParts p = gate_parts(g);
+    float hi = wave_incl_scan(p.hi, lane), lo = wave_incl_scan(p.lo, lane);
+    const float th = __shfl(hi, 63, 64), tl = __shfl(lo, 63, 64);
+    if (REV) {
+        hi = th - hi;
+        lo = tl - lo;
+    }
+    s.hi[lane] = hi;
+    s.lo[lane] = lo;
+    s.in[lane] = in_scale * exp2_hw(hi + lo);
+    s.out[lane] = up_scale * exp2_hw((th - hi) + (tl - lo));
+    if (lane == 0) s.dec = exp2_hw(th + tl);
+}
+
+// DA: elements of a and b, DC: of c.  TR: the state in memory is S^T ([K][V] with DA = V).
+// DOT: 1: the state's part of the output times x, for dg; 2: the pairs' sums as well.
+template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
+struct DecayBody {
+    typedef Eight<T> E8;
+    typedef typename E8::frag frag;
+    static constexpr int CT = DC / 64;        // column tiles of a wave
+    static constexpr int KT = DA / 16;        // row tiles of S
+    static constexpr int PW = 64 + 16 / sizeof(T);   // pitch of the pairs' rows
+    static constexpr bool SPREAD = CT == 2;
+
+    struct Shared {
+        T a[LOCAL ? 16 : 64 * DA], b[64 * DA], c[64 * DC], x[DOT ? 64 * DC : 16];
+        T pairs[LOCAL ? 16 : 64 * PW];
+        ChunkGates gates[2];
+        float dot[DOT ? 4 : 1][64], col[DOT == 2 ? 4 : 1][64], row[64];
+    };
+
+    // column (of c, out and S) of tile ct in lane group g, element e; CT = 2: the two tiles of
+    // a wave interleave by four columns, so that a lane holds eight in a row
+    __device__ __forceinline__ static int col0(int w, int g) { return w * (DC / 4) + (CT == 2 ? 8 : 4) * g; }
+
+    // offset of S tile (kt, ct)'s element e in the state's memory
+    __device__ __forceinline__ static int state_at(int w, int lane, int kt, int ct, int e) {
+        const int g = lane >> 4, r = lane & 15;
+        const int k = 32 * (kt >> 1) + 8 * g + 4 * (kt & 1) + e;
+        const int c = w * (DC / 4) + (SPREAD ? 8 * (r >> 2) + 4 * ct + (r & 3) : r);
+        return TR ? c * DA + k : k * DC + c;
+    }
+
+    __device__ static void run(const DecayWalk& p, Shared& s) {
+        const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g16 = lane >> 4, r16 = lane & 15;
+        const int64_t blk = blockIdx.x / p.H, h = blockIdx.x - blk * p.H;
+        const bool single = blk >= p.tiles;
+        Tile t;
+        if (single && p.map.seqs) {
+            const int4 q = p.map.seqs[blk - p.tiles];
+            t.row0 = __builtin_amdgcn_readfirstlane(q.x);
+            t.len = __builtin_amdgcn_readfirstlane(q.y);
+            if (t.len > p.map.tile) return;      // it has segments
+            t.n = t.len;
+            t.seq = (int)(blk - p.tiles);
+            t.j = 0;
+            t.nt = 1;
+        } else if (single) {
+            t = Tile{(blk - p.tiles) * p.map.T, (int)p.map.T, (int)(blk - p.tiles), 0, 1, (int)p.map.T};
+        } else {
+            t = tile_of(p.map, blk);
+            if (t.n == 0) return;
+            if (LOCAL && t.j == (REV ? 0 : t.nt - 1)) return;   // nothing follows it
+        }
+        const int nch = (t.n + 63) >> 6;
+        const int64_t KV = (int64_t)DA * DC;
+
+        const T* pa = LOCAL ? nullptr : static_cast<const T*>(p.a.p) + t.row0 * p.a.ts + (h / p.a.div) * p.a.hs;
+        const T* pb = static_cast<const T*>(p.b.p) + t.row0 * p.b.ts + (h / p.b.div) * p.b.hs;
+        const T* pc = static_cast<const T*>(p.c.p) + t.row0 * p.c.ts + (h / p.c.div) * p.c.hs;
+        const T* px = DOT ? static_cast<const T*>(p.x.p) + t.row0 * p.x.ts + (h / p.x.div) * p.x.hs : nullptr;
+        const float* pg = p.g + t.row0 * p.gs + h;
+
+        const Rows<T, DA> ra{s.a}, rb{s.b};
+        const Rows<T, DC> rc{s.c}, rx{s.x};
+        Ahead<T, DA> na, nb;
+        Ahead<T, DC> nc, nx;
+        const auto first_of = [&](int j) { return 64 * (REV ? nch - 1 - j : j); };   // j-th chunk walked
+        const auto fetch = [&](int j) {
+            const int64_t t0 = first_of(j);
+            const int n = min(64, t.n - (int)t0);
+            if (!LOCAL) na.load(pa + t0 * p.a.ts, p.a.ts, n, tid);
+            nb.load(pb + t0 * p.b.ts, p.b.ts, n, tid);
+            nc.load(pc + t0 * p.c.ts, p.c.ts, n, tid);
+            if (DOT) nx.load(px + t0 * p.x.ts, p.x.ts, n, tid);
+        };
+        const auto gate_of = [&](int j) {
+            const int at = first_of(j) + lane;
+            return at < t.n ? pg[at * p.gs] : 0.f;
+        };
+
+        f32x4 S[KT][CT];
+        const float* sin = LOCAL ? nullptr
+                           : single ? (p.seq_state ? p.seq_state + (t.seq * p.H + h) * KV : nullptr)
+                                    : p.tile_state + (blk * p.H + h) * KV;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                S[kt][ct] = zero4();
+                if (sin) {
+                    if constexpr (TR) {
+                        S[kt][ct] = *reinterpret_cast<const f32x4*>(sin + state_at(w, lane, kt, ct, 0));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[kt][ct][e] = sin[state_at(w, lane, kt, ct, e)];
+                    }
+                }
+            }
+        float total = 1.f;   // LOCAL: decay of the segment
+
+        constexpr int GW = REV ? 3 : 0;   // the wave with the fewest tiles of pairs makes the gates
+        float gnext = 0.f;
+        if (nch > 0) {
+            fetch(0);
+            if (w == GW) {
+                make_gates<REV>(s.gates[0], gate_of(0), p.in_scale, p.up_scale, lane);
+                if (nch > 1) gnext = gate_of(1);
+            }
+        }
+        for (int j = 0; j < nch; ++j) {
+            if (!LOCAL) na.put(ra, tid);
+            nb.put(rb, tid);
+            nc.put(rc, tid);
+            if (DOT) nx.put(rx, tid);
+            lds_barrier();
+            if (j + 1 < nch) fetch(j + 1);
+            const ChunkGates& gt = s.gates[j & 1];
+            if (w == GW && j + 1 < nch) {
+                make_gates<REV>(s.gates[(j + 1) & 1], gnext, p.in_scale, p.up_scale, lane);
+                if (j + 2 < nch) gnext = gate_of(j + 2);
+            }
+
+            // ---- pairs: tile row w of (a b^T), its transpose in the accumulators (rows b's tokens)
+            if constexpr (!LOCAL) {
+                const int i = 16 * w + r16;
+                frag af[DA / 32], xf[DOT == 2 ? DC / 32 : 1];
+#pragma unroll
+                for (int q = 0; q < DA / 32; ++q) af[q] = ra.row8(i, 32 * q + 8 * g16);
+                if constexpr (DOT == 2) {
+#pragma unroll
+                    for (int q = 0; q < DC / 32; ++q) xf[q] = rx.row8(i, 32 * q + 8 * g16);
+                }
+                const float hi = gt.hi[i], lo = gt.lo[i];
+                float rsum = 0.f;
+                // 32 columns of pairs at a time, as the products read them: past the diagonal only
+                // where their other half is needed
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    if (REV ? (jt | 1) < w : (jt & ~1) > w) continue;
+                    f32x4 P = zero4();
+                    if (REV ? jt >= w : jt <= w) {
+#pragma unroll
+                        for (int q = 0; q < DA / 32; ++q)
+                            P = E8::mma(rb.row8(16 * jt + r16, 32 * q + 8 * g16), af[q], P);
+                        const f32x4 jh = *reinterpret_cast<const f32x4*>(&gt.hi[16 * jt + 4 * g16]);
+                        const f32x4 jl = *reinterpret_cast<const f32x4*>(&gt.lo[16 * jt + 4 * g16]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int jj = 16 * jt + 4 * g16 + e;
+                            const float y = P[e] * (p.pair_scale * exp2_hw((hi - jh[e]) + (lo - jl[e])));
+                            P[e] = (REV ? jj >= i : jj <= i) ? y : 0.f;
+                        }
+                    }
+                    if constexpr (DOT == 2) {
+                        f32x4 M = zero4();
+                        if (jt <= w) {
+#pragma unroll
+                            for (int q = 0; q < DC / 32; ++q)
+                                M = E8::mma(rc.row8(16 * jt + r16, 32 * q + 8 * g16), xf[q], M);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                M[e] = 16 * jt + 4 * g16 + e < i ? M[e] * P[e] : 0.f;
+                                rsum += M[e];
+                            }
+                        }
+                        const f32x4 cs = row_sum16(M);
+                        if (r16 == 15) *reinterpret_cast<f32x4*>(&s.col[w][16 * jt + 4 * g16]) = cs;
+                    }
+                    store4(s.pairs + i * PW + 32 * (jt >> 1) + 8 * g16 + 4 * (jt & 1), P);
+                }
+                if constexpr (DOT == 2) {
+                    rsum = sum_groups(rsum);
+                    if (g16 == 0) s.row[i] = rsum;
+                    if (w < 2 && r16 == 15) {      // tiles that no pair of this row reaches
+                        *reinterpret_cast<f32x4*>(&s.col[w][32 + 4 * g16]) = zero4();
+                        *reinterpret_cast<f32x4*>(&s.col[w][48 + 4 * g16]) = zero4();
+                    }
+                }
+            }
+
+            // ---- the state's part: O^T = S^T a^T, rows the wave's columns, columns the tokens
+            f32x4 O[4][CT];
+            if constexpr (!LOCAL) {
+                constexpr int NP = DOT ? E8::PARTS : 1;
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) O[it][ct] = zero4();
+#pragma unroll
+                for (int q = 0; q < DA / 32; ++q) {
+                    frag sf[CT][NP];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = S[2 * q + (e >> 2)][ct][e & 3];
+                        E8::template split<NP>(f, sf[ct]);
+                    }
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const frag b = ra.row8(16 * it + r16, 32 * q + 8 * g16);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                            for (int n = 0; n < NP; ++n) O[it][ct] = E8::mma(sf[ct][n], b, O[it][ct]);
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int i = 16 * it + r16;
+                    const float f = gt.in[i];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) O[it][ct][e] *= f;
+                    if constexpr (DOT != 0) {
+                        const int c = col0(w, g16);
+                        float xv[8], d = 0.f;
+                        E8::unpack(rx.row8(i, c & ~7), xv);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                d += O[it][ct][e] * (CT == 2 ? xv[4 * ct + e] : (c & 4) ? xv[4 + e] : xv[e]);
+                        d = sum_groups(d);
+                        if (g16 == 0) s.dot[w][i] = d;
+                    }
+                }
+            }
+
+            // ---- the state: S <- dec S + b^T (out c)
+            frag cf[2][CT];
+#pragma unroll
+            for (int js = 0; js < 2; ++js)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    cf[js][ct] = rc.template col8<SPREAD>(32 * js, w * (DC / 4) + 4 * ct, lane);
+            const float dec = gt.dec;
+            if (LOCAL) total *= dec;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[kt][ct][e] *= dec;
+#pragma unroll
+            for (int js = 0; js < 2; ++js) {
+                frag cp[CT][E8::PARTS];
+                const f32x4 wl = *reinterpret_cast<const f32x4*>(&gt.out[32 * js + 4 * g16]);
+                const f32x4 wh = *reinterpret_cast<const f32x4*>(&gt.out[32 * js + 16 + 4 * g16]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    float f[8];
+                    E8::unpack(cf[js][ct], f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[e] *= wl[e];
+                        f[4 + e] *= wh[e];
+                    }
+                    E8::template split<E8::PARTS>(f, cp[ct]);
+                }
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    const frag b = rb.template col8<true>(32 * js, 32 * (kt >> 1) + 4 * (kt & 1), lane);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int n = 0; n < E8::PARTS; ++n) S[kt][ct] = E8::mma(b, cp[ct][n], S[kt][ct]);
+                }
+            }
+
+            if constexpr (!LOCAL) {
+                lds_barrier();   // the pairs of all tile rows are there
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int js = 0; js < 2; ++js) {
+                        if (REV ? 2 * js + 1 < it : 2 * js > it) continue;
+                        frag b;
+                        const T* q = s.pairs + (16 * it + r16) * PW + 32 * js + 8 * g16;
+                        if constexpr (sizeof(T) == 2) {
+                            b = *reinterpret_cast<const frag*>(q);
+                        } else {
+                            b = __builtin_shufflevector(reinterpret_cast<const f32x4*>(q)[0],
+                                                        reinterpret_cast<const f32x4*>(q)[1], 0, 1, 2, 3, 4, 5, 6, 7);
+                        }
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) O[it][ct] = E8::mma(cf[js][ct], b, O[it][ct]);
+                    }
+                const int64_t t0 = first_of(j);
+                const int n = min(64, t.n - (int)t0);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int i = 16 * it + r16;
+                    if (i >= n) continue;
+                    const int64_t at = ((t.row0 + t0 + i) * p.H + h) * DC + col0(w, g16);
+                    if (p.out32) {
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) store4(p.out32 + at + 4 * ct, O[it][ct]);
+                    } else {
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) store4(static_cast<T*>(p.out) + at + 4 * ct, O[it][ct]);
+                    }
+                }
+                if constexpr (DOT != 0) {
+                    if (tid < n) {
+                        float d = (s.dot[0][tid] + s.dot[1][tid]) + (s.dot[2][tid] + s.dot[3][tid]);
+                        if constexpr (DOT == 2)
+                            d += s.row[tid] - ((s.col[0][tid] + s.col[1][tid]) + (s.col[2][tid] + s.col[3][tid]));
+                        p.dots[h * p.tokens + t.row0 + t0 + tid] = d;
+                    }
+                }
+            }
+            lds_barrier();   // everything of this chunk has been read
+        }
+
+        float* sout = LOCAL ? p.local + (blk * p.H + h) * KV
+                      : (p.seq_out && t.j == (REV ? 0 : t.nt - 1)) ? p.seq_out + (t.seq * p.H + h) * KV : nullptr;
+        if (sout) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    if constexpr (TR) {
+                        *reinterpret_cast<f32x4*>(sout + state_at(w, lane, kt, ct, 0)) = S[kt][ct];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sout[state_at(w, lane, kt, ct, e)] = S[kt][ct][e];
+                    }
+                }
+        }
+        if (LOCAL && tid == 0) p.dec[blk * p.H + h] = total;
+        if constexpr (DOT == 2) {      // <S', E> at the segment's end
+            const float* e0 = single ? (p.seq_end ? p.seq_end + (t.seq * p.H + h) * KV : nullptr)
+                                     : p.tile_end + (blk * p.H + h) * KV;
+            float d = 0.f;
+            if (e0) {
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane, kt, ct, 0));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d += v[e] * S[kt][ct][e];
+                    }
+            }
+            d = wave_sum(d);
+            if (lane == 0) s.dot[w][0] = d;
+            __syncthreads();
+            if (tid == 0) p.ends[blk * p.H + h] = (s.dot[0][0] + s.dot[1][0]) + (s.dot[2][0] + s.dot[3][0]);
+        }
+    }
+};
+
+template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void decay_walk_kernel(DecayWalk p) {
+    typedef DecayBody<T, DA, DC, REV, TR, DOT, LOCAL> B;
+    __shared__ typename B::Shared s;
+    B::run(p, s);
+}
+
+template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
+hipError_t launch_walk(const DecayWalk& p) {
+    const int64_t blocks = (p.tiles + (LOCAL ? 0 : p.singles)) * p.H;
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)blocks), dim3(256), 0,
+                       p.stream, p);
+    return hipGetLastError();
+}
+
+// One walk for every type and head size: the launcher of a translation unit.
+template <bool REV, bool TR, int DOT, bool LOCAL>
+hipError_t launch_walk_of(const DecayWalk& p, int K, int V, bool bf) {
+#define GDN_DECAY_CASE(KK, VV)                                                                      \
+    if (K == KK && V == VV)                                                                         \
+        return bf ? launch_walk<bf16, TR ? VV : KK, TR ? KK : VV, REV, TR, DOT, LOCAL>(p)           \
+                  : launch_walk<float, TR ? VV : KK, TR ? KK : VV, REV, TR, DOT, LOCAL>(p);
+    GDN_DECAY_CASE(64, 64)
+    GDN_DECAY_CASE(64, 128)
+    GDN_DECAY_CASE(128, 64)
+    GDN_DECAY_CASE(128, 128)
+#undef GDN_DECAY_CASE
+    return hipErrorInvalidValue;
+}
+hipError_t launch_walk_o(const DecayWalk& p, int K, int V, bool bf);
+hipError_t launch_walk_dq(const DecayWalk& p, int K, int V, bool bf);
+hipError_t launch_walk_dk(const DecayWalk& p, int K, int V, bool bf);
+hipError_t launch_walk_dv(const DecayWalk& p, int K, int V, bool bf);
+hipError_t launch_walk_local(const DecayWalk& p, int K, int V, bool bf, bool rev);
+
+}  // namespace gdn

@@ -3,7 +3,10 @@
  * chunked forward, the single-token decode step and the chunked backward;
  * and the operators a layer puts around them: the gated linear recurrence
  * (gdn_linrec_*), the per-head norm of q and k with the position rotation
- * (gdn_qk_norm_rope*) and the short causal convolution (gdn_short_conv_*).
+ * (gdn_qk_norm_rope*) and the short causal convolution (gdn_short_conv_*);
+ * and the token mixers that alternate with it in a stack: linear attention
+ * with a decay per head (gdn_decay_attn_*) and attention over a paged cache
+ * (gdn_paged_append, gdn_paged_attn).
  *
  * The operation (the "gated delta rule"):
  *
@@ -53,7 +56,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 10
+#define GDN_ABI_VERSION 11
 
 typedef int32_t gdn_status;
 enum {
@@ -671,6 +674,150 @@ gdn_status gdn_short_conv_bwd(const gdn_conv_desc *d, const void *x, const float
  * [B, W-1, D] moves on by x in place. */
 gdn_status gdn_short_conv_step(const gdn_conv_desc *d, const void *x, const float *weight,
                                const float *bias, void *state, void *y, void *stream);
+
+/* ======================================================================
+ * Token mixers next to the delta rule.  The conventions above hold.
+ * ====================================================================== */
+
+/*
+ * Linear attention with a decay for each head, the delta rule without its
+ * correction:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T ,   o_t = scale q_t S_t ,
+ * states [K, V] float as the delta rule keeps them.  g is a natural-log gate
+ * for each token and state head, or one for each head that holds for all
+ * tokens (GDN_DECAY_PER_HEAD).  With num_v_heads = H_V, a multiple of H, state
+ * head h uses head h / (H_V / H) of q and k.  Any g is taken: a gate of
+ * -infinity (or below -104, where exp gives 0 in fp32) cuts the sequence, and
+ * growing gates are followed as far as their products stay finite.
+ *
+ * Rows of q, k and v may lie in wider tensors: a token stride and a head stride
+ * each (elements, multiples of 8; 0: dense).  Everything else is dense.
+ */
+enum { GDN_DECAY_PER_HEAD = 1 };
+typedef struct gdn_decay_desc {
+    int64_t batch;          /* B; must be 1 when cu_seqlens is given */
+    int64_t seq_len;        /* T: tokens per sequence, or all packed tokens */
+    int64_t num_heads;      /* H: heads of q and k */
+    int64_t num_v_heads;    /* H_V: heads of v, g, o and the states; 0: H */
+    int64_t key_dim;        /* K: 64 or 128 */
+    int64_t value_dim;      /* V: 64 or 128 */
+    int64_t num_seqs;       /* N packed sequences when cu_seqlens is given, else 0 */
+    int64_t q_stride, k_stride, v_stride;                   /* token strides */
+    int64_t q_head_stride, k_head_stride, v_head_stride;
+    int32_t dtype;          /* GDN_DTYPE_* of q, k, v, o and their gradients */
+    int32_t flags;          /* GDN_DECAY_* */
+    float scale;
+} gdn_decay_desc;
+
+/* Bytes of workspace of gdn_decay_attn_fwd (backward = 0) or _bwd (1); may be 0. */
+gdn_status gdn_decay_attn_workspace(const gdn_decay_desc *d, int32_t backward, size_t *bytes);
+
+/*
+ *   q, k  [B, T, H, K], v [B, T, H_V, V], 16-byte aligned
+ *   g     [B, T, H_V] float, or [H_V] with GDN_DECAY_PER_HEAD
+ *   h0    [N, H_V, K, V] float, initial state, NULL: zeros
+ *   o     [B, T, H_V, V], output
+ *   ht    [N, H_V, K, V] float, final state (h0 of an empty sequence); NULL:
+ *         not returned.  ht may equal h0.
+ * N = B without cu_seqlens, num_seqs with it.  States are 16-byte aligned.
+ */
+gdn_status gdn_decay_attn_fwd(const gdn_decay_desc *d, const void *q, const void *k, const void *v,
+                              const float *g, const float *h0, const int64_t *cu_seqlens,
+                              void *o, float *ht, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * Gradients of <dout, o> + <dht, ht>.  With E_t the gradient of S_t:
+ *   E_t = exp(g_{t+1}) E_{t+1} + scale q_t dout_t^T  (that of a last token: dht + ...),
+ *   dq_t = scale S_t dout_t, dk_t = E_t v_t, dv_t = E_t^T k_t,
+ *   dg_t = exp(g_t) <S_{t-1}, E_t>, summed over the tokens with GDN_DECAY_PER_HEAD;
+ * dq and dk of a head sum the terms of the H_V / H state heads that use it.
+ *   dout   [B, T, H_V, V];  dht [N, H_V, K, V] float or NULL
+ *   dq, dk [B, T, H, K], dv [B, T, H_V, V], dg (shape of g, float), written
+ *   dh0    [N, H_V, K, V] float, written, or NULL
+ * Nothing is kept from a forward call.  Sums are taken in a fixed order: the
+ * same call gives the same bits.
+ */
+gdn_status gdn_decay_attn_bwd(const gdn_decay_desc *d, const void *q, const void *k, const void *v,
+                              const float *g, const float *h0, const int64_t *cu_seqlens,
+                              const void *dout, const float *dht,
+                              void *dq, void *dk, void *dv, float *dg, float *dh0,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of batch sequences (seq_len 1, num_seqs 0; batch may be 0): state
+ * [B, H_V, K, V] is updated in place, o [B, H_V, V] written. */
+gdn_status gdn_decay_attn_step(const gdn_decay_desc *d, const void *q, const void *k, const void *v,
+                               const float *g, float *state, void *o, void *stream);
+
+/*
+ * A paged cache: k_cache and v_cache are pools of `pages` pages of page_size
+ * tokens, element (page, slot, head, d) at page * page_stride + slot *
+ * token_stride + head * head_stride + d (strides in elements, multiples of 8,
+ * rows must not overlap): pages of [slot][head], of [head][slot], or keys and
+ * values of a page next to each other.  Position p of sequence n is slot
+ * p % page_size of page page_table[n][p / page_size].  A position outside the
+ * table's row, or whose entry is not in 0 .. pages - 1, is not there: nothing
+ * is written to it and nothing attends to it.
+ */
+typedef struct gdn_pages {
+    int64_t num_seqs;       /* N: rows of page_table */
+    int64_t max_pages;      /* entries of a row; max_pages * page_size below 2^31 */
+    int64_t pages;          /* of the pool */
+    int64_t page_size;      /* tokens of a page, >= 1 */
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+} gdn_pages;
+
+/*
+ * Appends tokens: k with the norm and the rotation of gdn_qk_norm_rope and v as
+ * it is go to positions lens[n] + t (t-th token of sequence n in this call), and
+ * q, where one is given, is normed and rotated alike into q_out.
+ *   d           as for gdn_qk_norm_rope; batch rows are the sequences, or, with
+ *               cu_seqlens [N + 1], batch 1 holds N packed ones
+ *   q [B, T, Hq, D] with q_out dense alike, or both NULL;  k, v [B, T, Hk, D]
+ *   v_stride, v_head_stride   of v, multiples of 8 (0: dense)
+ *   positions   [B, T] int64 for the rotation, NULL: lens[n] + t
+ *   lens        [N] int64, tokens that the cache holds; not changed.  A negative
+ *               one, or one past the table, leaves its sequence's pages alone.
+ * Offsets outside [0, T] leave tokens unwritten.  Two tokens for one slot
+ * (sequences that share a page) leave one of the two.
+ */
+gdn_status gdn_paged_append(const gdn_qk_desc *d, const gdn_pages *c, const void *q, const void *k,
+                            const void *v, int64_t v_stride, int64_t v_head_stride,
+                            const float *q_weight, const float *k_weight, const double *inv_freq,
+                            const int64_t *positions, const int64_t *cu_seqlens,
+                            const int32_t *page_table, const int64_t *lens,
+                            void *q_out, void *k_cache, void *v_cache, void *stream);
+
+/*
+ * Attention of one new token of each sequence over its cached ones:
+ *   o = softmax(scale q K^T) V  over positions max(0, lens[n] - window) .. lens[n] - 1
+ * (window 0: from 0), with key head h / (q_heads / k_heads) for query head h.
+ * A sequence with nothing to attend to (lens[n] <= 0, or no page there) gets zeros;
+ * lens past the table count up to its end.
+ */
+typedef struct gdn_paged_attn_desc {
+    int64_t num_seqs;       /* N, may be 0 */
+    int64_t q_heads;        /* a multiple of k_heads */
+    int64_t k_heads;
+    int64_t head_dim;       /* D: a multiple of 8 up to 256 */
+    int64_t q_stride;       /* strides of q between sequences and heads (0: dense) */
+    int64_t q_head_stride;
+    int64_t window;
+    int32_t dtype;          /* GDN_DTYPE_* of q, the caches and o */
+    float scale;
+} gdn_paged_attn_desc;
+
+gdn_status gdn_paged_attn_workspace(const gdn_paged_attn_desc *d, size_t *bytes);
+
+/*
+ *   q [N, Hq, D], o [N, Hq, D] (dense, written), 16-byte aligned
+ *   page_table [N, max_pages] int32, lens [N] int64, device memory
+ */
+gdn_status gdn_paged_attn(const gdn_paged_attn_desc *d, const gdn_pages *c, const void *q,
+                          const void *k_cache, const void *v_cache, const int32_t *page_table,
+                          const int64_t *lens, void *o, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 #ifdef __cplusplus
 }
