@@ -32,6 +32,8 @@ gdn_status check_decay(const gdn_decay_desc* d, bool packed) {
             return api_fail(GDN_ERR_BAD_SHAPE, "head stride %lld, token stride %lld: rows overlap", (long long)hs[i],
                             (long long)ts[i]);
         if (h % 8 || ts[i] % 8) return api_fail(GDN_ERR_MISALIGNED, "strides must be multiples of 8 elements");
+        if (ts[i] >= 1 << 24 || H[i] * h >= 1 << 24)   // offsets inside a chunk of 64 rows are 32-bit
+            return api_fail(GDN_ERR_BAD_SHAPE, "token stride %lld: below 2^24 elements", (long long)(ts[i] ? ts[i] : H[i] * h));
     }
     return GDN_OK;
 }

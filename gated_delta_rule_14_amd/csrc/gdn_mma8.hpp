@@ -62,25 +62,28 @@ template <> struct Eight<float> {
     }
 };
 
-// 64 rows of D elements in LDS, 16-byte units of a row permuted by the row's
-// number: rows of one column of units then lie in different banks.
+// Rows of D elements in LDS, 16 bytes apart beyond their width: rows of one column
+// then start in different banks, and every address is one register and a constant.
+// The gap of a row holds four floats for whoever wants them.
 template <typename T, int D> struct Rows {
-    static constexpr int U = 16 / sizeof(T), UR = D / U, PER = 64 * UR / 256;
+    static constexpr int U = 16 / sizeof(T), UR = D / U, PITCH = D + U;
     typedef typename Eight<T>::frag frag;
     T* p;
-    __device__ __forceinline__ static int at(int row, int unit) {
-        const int f = UR >= 16 ? row & 15 : (row >> 1) & 7;
-        return row * D + (unit ^ f) * U;
-    }
+    __device__ __forceinline__ static int at(int row, int d) { return row * PITCH + d; }
+    __device__ __forceinline__ float* gap(int row) const { return reinterpret_cast<float*>(p + at(row, D)); }
     // elements d .. d+7 of a row (d a multiple of 8)
     __device__ __forceinline__ frag row8(int row, int d) const {
         if constexpr (sizeof(T) == 2) {
-            return *reinterpret_cast<const frag*>(p + at(row, d >> 3));
+            return *reinterpret_cast<const frag*>(p + at(row, d));
         } else {
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(p + at(row, d >> 2));
-            const f32x4 hi = *reinterpret_cast<const f32x4*>(p + at(row, (d >> 2) + 1));
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(p + at(row, d));
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(p + at(row, d + 4));
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
+    }
+    // elements d .. d+3 of a row in fp32 (d a multiple of 4)
+    __device__ __forceinline__ f32x4 row4(int row, int d) const {
+        return Quad<T>::get(Quad<T>::load(p + at(row, d)));
     }
     // Transposed: lane r of a group of 16 gets column d0 + 8 (r / 4) + r % 4 (d0 a multiple of
     // 4; SPREAD false: d0 + r) at rows t0 + 4g + 0..3 and t0 + 16 + 4g + 0..3.
@@ -91,8 +94,8 @@ template <typename T, int D> struct Rows {
             const int row = t0 + 4 * g + (r >> 2), d = d0 + (SPREAD ? 8 : 4) * (r & 3);
             typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
             typedef short i16x8 __attribute__((ext_vector_type(8)));
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + at(row, d >> 3) + (d & 4)));
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + at(row + 16, d >> 3) + (d & 4)));
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + at(row, d)));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + at(row + 16, d)));
             return __builtin_bit_cast(frag, (i16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             const int d = d0 + (SPREAD ? 8 * (r >> 2) + (r & 3) : r);
@@ -100,7 +103,7 @@ template <typename T, int D> struct Rows {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int row = t0 + 4 * g + (e & 3) + 4 * (e & 4);
-                v[e] = p[at(row, d >> 2) + (d & 3)];
+                v[e] = p[at(row, d)];
             }
             return v;
         }

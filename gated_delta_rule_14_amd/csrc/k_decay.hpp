@@ -19,9 +19,8 @@
 // R and C the row and column sums of the pairs (q_i k_j)(do_i v_j) e^{G_i-G_j},
 // j < i: sums of decayed terms only, so strong decays keep their digits.
 //
-// A workgroup of four waves walks the chunks of one segment of one head.  The
-// waves own a quarter of the columns of c and S each; S stays in MFMA
-// accumulators, whose layout is that of an operand over its own rows, so S
+// A workgroup walks the chunks of one segment of one head.  Each of its waves
+// owns 16 columns of c and S; S stays in MFMA accumulators, whose layout is that of an operand over its own rows, so S
 // never passes through LDS.  The pairs' products of the chunk are made once,
 // a tile row to a wave, and handed round in LDS.  Long sequences are cut into
 // segments: a first walk makes each segment's own state, launch_decay_join
@@ -39,23 +38,25 @@
 
 namespace gdn {
 
-// A chunk's rows on their way from memory to LDS: PER 16-byte units to a thread.
-template <typename T, int D> struct Ahead {
+// A chunk's rows on their way from memory to LDS: PER 16-byte units to each of NT threads.
+// Past the chunk's n rows the last one is read again (the gates give those rows no
+// weight).  Addresses are the rows' base in scalar registers and a 32-bit offset:
+// token strides are below 2^24 elements.
+template <typename T, int D, int NT> struct Ahead {
     typedef Rows<T, D> R;
-    u32x4 u[R::PER];
-    __device__ __forceinline__ void load(const T* base, int64_t ts, int n, int tid) {
+    static constexpr int STEP = NT / R::UR, PER = 64 / STEP;     // rows between a thread's units
+    u32x4 u[PER];
+    __device__ __forceinline__ void load(const T* base, unsigned ts, int n, int tid) {
+        const unsigned tb = ts * sizeof(T), row = tid / R::UR * tb, unit = tid % R::UR * 16, last = (n - 1) * tb;
+        const T* p = in_scalar(base);
 #pragma unroll
-        for (int i = 0; i < R::PER; ++i) {
-            const int q = tid + 256 * i, row = q / R::UR, unit = q % R::UR;
-            u[i] = u32x4{0, 0, 0, 0};
-            if (row < n) u[i] = *reinterpret_cast<const u32x4*>(base + row * ts + unit * R::U);
-        }
+        for (int i = 0; i < PER; ++i) u[i] = peek_row<u32x4>(p, min(row + STEP * i * tb, last) + unit);
     }
     __device__ __forceinline__ void put(const R& r, int tid) const {
 #pragma unroll
-        for (int i = 0; i < R::PER; ++i) {
-            const int q = tid + 256 * i;
-            *reinterpret_cast<u32x4*>(r.p + R::at(q / R::UR, q % R::UR)) = u[i];
+        for (int i = 0; i < PER; ++i) {
+            const int q = tid + NT * i;
+            *reinterpret_cast<u32x4*>(r.p + R::at(q / R::UR, q % R::UR * R::U)) = u[i];
         }
     }
 };
@@ -75,25 +76,43 @@ __device__ __forceinline__ GateParts gate_parts(float g) {
     return {h, fmaf(g, LOG2E, -h)};   // NaN stays one
 }
 
+// Inclusive prefix sum over the wave's 64 lanes, by DPP row shifts and broadcasts.
+template <int CTRL, int MASK> __device__ __forceinline__ float dpp_from(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, MASK, 0xf, false));
+}
+__device__ __forceinline__ float scan64(float x) {
+    x = dpp_from<0x111, 0xf>(x);   // row_shr:1, 2, 4, 8
+    x = dpp_from<0x112, 0xf>(x);
+    x = dpp_from<0x114, 0xf>(x);
+    x = dpp_from<0x118, 0xf>(x);
+    x = dpp_from<0x142, 0xa>(x);   // row_bcast:15 into rows 1 and 3
+    x = dpp_from<0x143, 0xc>(x);   // row_bcast:31 into rows 2 and 3
+    return x;
+}
+
 // What the waves need of a chunk's gates: sums up to each token (reversed walks:
 // from behind it), the factors of the state in and out, and of the whole chunk.
+// Rows past the chunk's n tokens get sums that give every pair with them the weight
+// 0, and factors of 0.
 struct alignas(16) ChunkGates {
     float hi[64], lo[64], in[64], out[64];
     float dec;
 };
 template <bool REV>
-__device__ __forceinline__ void make_gates(ChunkGates& s, float g, float in_scale, float up_scale, int lane) {
-    const GateParts p = gate_parts(g);
-    float hi = wave_incl_scan(p.hi, lane), lo = wave_incl_scan(p.lo, lane);
-    const float th = __shfl(hi, 63, 64), tl = __shfl(lo, 63, 64);
+__device__ __forceinline__ void make_gates(ChunkGates& s, float g, int n, float in_scale, float up_scale, int lane) {
+    const bool on = lane < n;
+    const GateParts p = gate_parts(on ? g : 0.f);
+    float hi = scan64(p.hi), lo = scan64(p.lo);
+    const float th = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), 63));
+    const float tl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), 63));
     if (REV) {
         hi = th - hi;
         lo = tl - lo;
     }
-    s.hi[lane] = hi;
+    s.hi[lane] = on ? hi : REV ? 8192.f * 64 : -8192.f * 64;
     s.lo[lane] = lo;
-    s.in[lane] = in_scale * exp2_hw(hi + lo);
-    s.out[lane] = up_scale * exp2_hw((th - hi) + (tl - lo));
+    s.in[lane] = on ? in_scale * exp2_hw(hi + lo) : 0.f;
+    s.out[lane] = on ? up_scale * exp2_hw((th - hi) + (tl - lo)) : 0.f;
     if (lane == 0) s.dec = exp2_hw(th + tl);
 }
 
@@ -103,27 +122,23 @@ template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
 struct DecayBody {
     typedef Eight<T> E8;
     typedef typename E8::frag frag;
-    static constexpr int CT = DC / 64;        // column tiles of a wave
+    static constexpr int W = DC / 16;         // waves: 16 columns each
     static constexpr int KT = DA / 16;        // row tiles of S
     static constexpr int PW = 64 + 16 / sizeof(T);   // pitch of the pairs' rows
-    static constexpr bool SPREAD = CT == 2;
 
+    // the gaps of the rows hold the sums for dg: a's and b's those of the waves' columns, c's
+    // the pairs' column sums, x's their row sums
     struct Shared {
-        T a[LOCAL ? 16 : 64 * DA], b[64 * DA], c[64 * DC], x[DOT ? 64 * DC : 16];
+        T a[LOCAL ? 16 : 64 * Rows<T, DA>::PITCH], b[64 * Rows<T, DA>::PITCH], c[64 * Rows<T, DC>::PITCH];
+        T x[DOT ? 64 * Rows<T, DC>::PITCH : 16];
         T pairs[LOCAL ? 16 : 64 * PW];
         ChunkGates gates[2];
-        float dot[DOT ? 4 : 1][64], col[DOT == 2 ? 4 : 1][64], row[64];
+        float ends[8];
     };
 
-    // column (of c, out and S) of tile ct in lane group g, element e; CT = 2: the two tiles of
-    // a wave interleave by four columns, so that a lane holds eight in a row
-    __device__ __forceinline__ static int col0(int w, int g) { return w * (DC / 4) + (CT == 2 ? 8 : 4) * g; }
-
-    // offset of S tile (kt, ct)'s element e in the state's memory
-    __device__ __forceinline__ static int state_at(int w, int lane, int kt, int ct, int e) {
-        const int g = lane >> 4, r = lane & 15;
-        const int k = 32 * (kt >> 1) + 8 * g + 4 * (kt & 1) + e;
-        const int c = w * (DC / 4) + (SPREAD ? 8 * (r >> 2) + 4 * ct + (r & 3) : r);
+    // offset of S tile kt's element e in the state's memory
+    __device__ __forceinline__ static int state_at(int w, int lane, int kt, int e) {
+        const int k = 32 * (kt >> 1) + 8 * (lane >> 4) + 4 * (kt & 1) + e, c = 16 * w + (lane & 15);
         return TR ? c * DA + k : k * DC + c;
     }
 
@@ -159,48 +174,46 @@ struct DecayBody {
 
         const Rows<T, DA> ra{s.a}, rb{s.b};
         const Rows<T, DC> rc{s.c}, rx{s.x};
-        Ahead<T, DA> na, nb;
-        Ahead<T, DC> nc, nx;
+        Ahead<T, DA, 64 * W> na, nb;
+        Ahead<T, DC, 64 * W> nc, nx;
         const auto first_of = [&](int j) { return 64 * (REV ? nch - 1 - j : j); };   // j-th chunk walked
         const auto fetch = [&](int j) {
             const int64_t t0 = first_of(j);
             const int n = min(64, t.n - (int)t0);
-            if (!LOCAL) na.load(pa + t0 * p.a.ts, p.a.ts, n, tid);
-            nb.load(pb + t0 * p.b.ts, p.b.ts, n, tid);
-            nc.load(pc + t0 * p.c.ts, p.c.ts, n, tid);
-            if (DOT) nx.load(px + t0 * p.x.ts, p.x.ts, n, tid);
+            if (!LOCAL) na.load(pa + t0 * p.a.ts, (unsigned)p.a.ts, n, tid);
+            nb.load(pb + t0 * p.b.ts, (unsigned)p.b.ts, n, tid);
+            nc.load(pc + t0 * p.c.ts, (unsigned)p.c.ts, n, tid);
+            if (DOT) nx.load(px + t0 * p.x.ts, (unsigned)p.x.ts, n, tid);
         };
         const auto gate_of = [&](int j) {
-            const int at = first_of(j) + lane;
-            return at < t.n ? pg[at * p.gs] : 0.f;
+            const int at = min(first_of(j) + lane, t.n - 1);
+            return pg[at * p.gs];
         };
 
-        f32x4 S[KT][CT];
+        f32x4 S[KT];
         const float* sin = LOCAL ? nullptr
                            : single ? (p.seq_state ? p.seq_state + (t.seq * p.H + h) * KV : nullptr)
                                     : p.tile_state + (blk * p.H + h) * KV;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt) {
+            S[kt] = zero4();
+            if (sin) {
+                if constexpr (TR) {
+                    S[kt] = *reinterpret_cast<const f32x4*>(sin + state_at(w, lane, kt, 0));
+                } else {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                S[kt][ct] = zero4();
-                if (sin) {
-                    if constexpr (TR) {
-                        S[kt][ct] = *reinterpret_cast<const f32x4*>(sin + state_at(w, lane, kt, ct, 0));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) S[kt][ct][e] = sin[state_at(w, lane, kt, ct, e)];
-                    }
+                    for (int e = 0; e < 4; ++e) S[kt][e] = sin[state_at(w, lane, kt, e)];
                 }
             }
+        }
         float total = 1.f;   // LOCAL: decay of the segment
 
-        constexpr int GW = REV ? 3 : 0;   // the wave with the fewest tiles of pairs makes the gates
+        constexpr int GW = REV ? W - 1 : 0;   // a wave with few or no pairs makes the gates
         float gnext = 0.f;
         if (nch > 0) {
             fetch(0);
             if (w == GW) {
-                make_gates<REV>(s.gates[0], gate_of(0), p.in_scale, p.up_scale, lane);
+                make_gates<REV>(s.gates[0], gate_of(0), t.n - first_of(0), p.in_scale, p.up_scale, lane);
                 if (nch > 1) gnext = gate_of(1);
             }
         }
@@ -213,93 +226,92 @@ struct DecayBody {
             if (j + 1 < nch) fetch(j + 1);
             const ChunkGates& gt = s.gates[j & 1];
             if (w == GW && j + 1 < nch) {
-                make_gates<REV>(s.gates[(j + 1) & 1], gnext, p.in_scale, p.up_scale, lane);
+                make_gates<REV>(s.gates[(j + 1) & 1], gnext, t.n - first_of(j + 1), p.in_scale, p.up_scale, lane);
                 if (j + 2 < nch) gnext = gate_of(j + 2);
             }
 
-            // ---- pairs: tile row w of (a b^T), its transpose in the accumulators (rows b's tokens)
+            // ---- pairs: 16 rows and 64 (8 waves: 32) columns of a b^T to a wave, transposed in the
+            // accumulators (rows b's tokens); blocks of 32 columns beyond the diagonal are never read
             if constexpr (!LOCAL) {
-                const int i = 16 * w + r16;
-                frag af[DA / 32], xf[DOT == 2 ? DC / 32 : 1];
-#pragma unroll
-                for (int q = 0; q < DA / 32; ++q) af[q] = ra.row8(i, 32 * q + 8 * g16);
-                if constexpr (DOT == 2) {
-#pragma unroll
-                    for (int q = 0; q < DC / 32; ++q) xf[q] = rx.row8(i, 32 * q + 8 * g16);
-                }
-                const float hi = gt.hi[i], lo = gt.lo[i];
+                constexpr int NJ = W == 8 ? 2 : 4;                     // tiles of a wave
+                const int it = W == 8 ? w >> 1 : w, j0 = W == 8 ? 2 * (w & 1) : 0;
+                const int i = 16 * it + r16;
                 float rsum = 0.f;
-                // 32 columns of pairs at a time, as the products read them: past the diagonal only
-                // where their other half is needed
+                if (W == 4 || (REV ? j0 + 1 >= it : j0 <= it)) {
+                    frag af[DA / 32], xf[DOT == 2 ? DC / 32 : 1];
 #pragma unroll
-                for (int jt = 0; jt < 4; ++jt) {
-                    if (REV ? (jt | 1) < w : (jt & ~1) > w) continue;
-                    f32x4 P = zero4();
-                    if (REV ? jt >= w : jt <= w) {
-#pragma unroll
-                        for (int q = 0; q < DA / 32; ++q)
-                            P = E8::mma(rb.row8(16 * jt + r16, 32 * q + 8 * g16), af[q], P);
-                        const f32x4 jh = *reinterpret_cast<const f32x4*>(&gt.hi[16 * jt + 4 * g16]);
-                        const f32x4 jl = *reinterpret_cast<const f32x4*>(&gt.lo[16 * jt + 4 * g16]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int jj = 16 * jt + 4 * g16 + e;
-                            const float y = P[e] * (p.pair_scale * exp2_hw((hi - jh[e]) + (lo - jl[e])));
-                            P[e] = (REV ? jj >= i : jj <= i) ? y : 0.f;
-                        }
-                    }
+                    for (int q = 0; q < DA / 32; ++q) af[q] = ra.row8(i, 32 * q + 8 * g16);
                     if constexpr (DOT == 2) {
-                        f32x4 M = zero4();
-                        if (jt <= w) {
 #pragma unroll
-                            for (int q = 0; q < DC / 32; ++q)
-                                M = E8::mma(rc.row8(16 * jt + r16, 32 * q + 8 * g16), xf[q], M);
+                        for (int q = 0; q < DC / 32; ++q) xf[q] = rx.row8(i, 32 * q + 8 * g16);
+                    }
+                    const float hi = gt.hi[i], lo = gt.lo[i];
+#pragma unroll
+                    for (int u = 0; u < NJ; ++u) {
+                        const int jt = j0 + u;
+                        if (REV ? (jt | 1) < it : (jt & ~1) > it) continue;
+                        f32x4 P = zero4();
+                        if (REV ? jt >= it : jt <= it) {
+#pragma unroll
+                            for (int q = 0; q < DA / 32; ++q)
+                                P = E8::mma(rb.row8(16 * jt + r16, 32 * q + 8 * g16), af[q], P);
+                            const f32x4 jh = *reinterpret_cast<const f32x4*>(&gt.hi[16 * jt + 4 * g16]);
+                            const f32x4 jl = *reinterpret_cast<const f32x4*>(&gt.lo[16 * jt + 4 * g16]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                M[e] = 16 * jt + 4 * g16 + e < i ? M[e] * P[e] : 0.f;
-                                rsum += M[e];
+                                const int jj = 16 * jt + 4 * g16 + e;
+                                const float y = P[e] * (p.pair_scale * exp2_hw((hi - jh[e]) + (lo - jl[e])));
+                                P[e] = (REV ? jj >= i : jj <= i) ? y : 0.f;
                             }
                         }
-                        const f32x4 cs = row_sum16(M);
-                        if (r16 == 15) *reinterpret_cast<f32x4*>(&s.col[w][16 * jt + 4 * g16]) = cs;
+                        if constexpr (DOT == 2) {
+                            f32x4 M = zero4();
+                            if (jt <= it) {
+#pragma unroll
+                                for (int q = 0; q < DC / 32; ++q)
+                                    M = E8::mma(rc.row8(16 * jt + r16, 32 * q + 8 * g16), xf[q], M);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    M[e] = 16 * jt + 4 * g16 + e < i ? M[e] * P[e] : 0.f;
+                                    rsum += M[e];
+                                }
+                            }
+                            const f32x4 cs = row_sum16(M);
+                            if (r16 == 15) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) rc.gap(16 * jt + 4 * g16 + e)[it] = cs[e];
+                            }
+                        }
+                        store4(s.pairs + i * PW + 32 * (jt >> 1) + 8 * g16 + 4 * (jt & 1), P);
                     }
-                    store4(s.pairs + i * PW + 32 * (jt >> 1) + 8 * g16 + 4 * (jt & 1), P);
                 }
                 if constexpr (DOT == 2) {
                     rsum = sum_groups(rsum);
-                    if (g16 == 0) s.row[i] = rsum;
-                    if (w < 2 && r16 == 15) {      // tiles that no pair of this row reaches
-                        *reinterpret_cast<f32x4*>(&s.col[w][32 + 4 * g16]) = zero4();
-                        *reinterpret_cast<f32x4*>(&s.col[w][48 + 4 * g16]) = zero4();
-                    }
+                    if (g16 == 0) rx.gap(i)[W == 8 ? w & 1 : 0] = rsum;
+                    if (W == 4 && g16 == 0) rx.gap(i)[1] = 0.f;
+                    if (it < 2 && (W == 4 || j0 == 2) && lane < 32) rc.gap(32 + lane)[it] = 0.f;   // no pairs of these rows
                 }
             }
 
+            __builtin_amdgcn_sched_barrier(0);   // phases kept apart: fewer registers at once
             // ---- the state's part: O^T = S^T a^T, rows the wave's columns, columns the tokens
-            f32x4 O[4][CT];
+            f32x4 O[4];
             if constexpr (!LOCAL) {
                 constexpr int NP = DOT ? E8::PARTS : 1;
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) O[it][ct] = zero4();
+                for (int it = 0; it < 4; ++it) O[it] = zero4();
 #pragma unroll
                 for (int q = 0; q < DA / 32; ++q) {
-                    frag sf[CT][NP];
+                    frag sf[NP];
+                    float f[8];
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = S[2 * q + (e >> 2)][ct][e & 3];
-                        E8::template split<NP>(f, sf[ct]);
-                    }
+                    for (int e = 0; e < 8; ++e) f[e] = S[2 * q + (e >> 2)][e & 3];
+                    E8::template split<NP>(f, sf);
 #pragma unroll
                     for (int it = 0; it < 4; ++it) {
                         const frag b = ra.row8(16 * it + r16, 32 * q + 8 * g16);
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                            for (int n = 0; n < NP; ++n) O[it][ct] = E8::mma(sf[ct][n], b, O[it][ct]);
+                        for (int n = 0; n < NP; ++n) O[it] = E8::mma(sf[n], b, O[it]);
                     }
                 }
 #pragma unroll
@@ -307,62 +319,47 @@ struct DecayBody {
                     const int i = 16 * it + r16;
                     const float f = gt.in[i];
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) O[it][ct][e] *= f;
+                    for (int e = 0; e < 4; ++e) O[it][e] *= f;
                     if constexpr (DOT != 0) {
-                        const int c = col0(w, g16);
-                        float xv[8], d = 0.f;
-                        E8::unpack(rx.row8(i, c & ~7), xv);
+                        const f32x4 xv = rx.row4(i, 16 * w + 4 * g16);
+                        float d = 0.f;
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                d += O[it][ct][e] * (CT == 2 ? xv[4 * ct + e] : (c & 4) ? xv[4 + e] : xv[e]);
+                        for (int e = 0; e < 4; ++e) d += O[it][e] * xv[e];
                         d = sum_groups(d);
-                        if (g16 == 0) s.dot[w][i] = d;
+                        if (g16 == 0) (w < 4 ? ra : rb).gap(i)[w & 3] = d;
                     }
                 }
             }
 
+            __builtin_amdgcn_sched_barrier(0);
             // ---- the state: S <- dec S + b^T (out c)
-            frag cf[2][CT];
+            frag cf[2];
 #pragma unroll
-            for (int js = 0; js < 2; ++js)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    cf[js][ct] = rc.template col8<SPREAD>(32 * js, w * (DC / 4) + 4 * ct, lane);
+            for (int js = 0; js < 2; ++js) cf[js] = rc.template col8<false>(32 * js, 16 * w, lane);
             const float dec = gt.dec;
             if (LOCAL) total *= dec;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) S[kt][ct][e] *= dec;
+                for (int e = 0; e < 4; ++e) S[kt][e] *= dec;
 #pragma unroll
             for (int js = 0; js < 2; ++js) {
-                frag cp[CT][E8::PARTS];
+                frag cp[E8::PARTS];
                 const f32x4 wl = *reinterpret_cast<const f32x4*>(&gt.out[32 * js + 4 * g16]);
                 const f32x4 wh = *reinterpret_cast<const f32x4*>(&gt.out[32 * js + 16 + 4 * g16]);
+                float f[8];
+                E8::unpack(cf[js], f);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    float f[8];
-                    E8::unpack(cf[js][ct], f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[e] *= wl[e];
-                        f[4 + e] *= wh[e];
-                    }
-                    E8::template split<E8::PARTS>(f, cp[ct]);
+                for (int e = 0; e < 4; ++e) {
+                    f[e] *= wl[e];
+                    f[4 + e] *= wh[e];
                 }
+                E8::template split<E8::PARTS>(f, cp);
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     const frag b = rb.template col8<true>(32 * js, 32 * (kt >> 1) + 4 * (kt & 1), lane);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                        for (int n = 0; n < E8::PARTS; ++n) S[kt][ct] = E8::mma(b, cp[ct][n], S[kt][ct]);
+                    for (int n = 0; n < E8::PARTS; ++n) S[kt] = E8::mma(b, cp[n], S[kt]);
                 }
             }
 
@@ -381,29 +378,33 @@ struct DecayBody {
                             b = __builtin_shufflevector(reinterpret_cast<const f32x4*>(q)[0],
                                                         reinterpret_cast<const f32x4*>(q)[1], 0, 1, 2, 3, 4, 5, 6, 7);
                         }
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) O[it][ct] = E8::mma(cf[js][ct], b, O[it][ct]);
+                        O[it] = E8::mma(cf[js], b, O[it]);
                     }
                 const int64_t t0 = first_of(j);
                 const int n = min(64, t.n - (int)t0);
+                const int64_t first = ((t.row0 + t0) * p.H + h) * DC;
+                unsigned at = (unsigned)r16 * (unsigned)(p.H * DC) + 16 * w + 4 * g16;
+                asm volatile("" : "+v"(at));   // (a 64-bit form of it would be kept over the loop)
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
-                    const int i = 16 * it + r16;
-                    if (i >= n) continue;
-                    const int64_t at = ((t.row0 + t0 + i) * p.H + h) * DC + col0(w, g16);
-                    if (p.out32) {
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) store4(p.out32 + at + 4 * ct, O[it][ct]);
+                    if (r16 >= n - 16 * it) continue;
+                    const int64_t row = first + 16 * it * p.H * DC;
+                    if (sizeof(T) == 4 || p.out32) {
+                        poke_row(in_scalar((p.out32 ? p.out32 : static_cast<float*>(p.out)) + row), at * 4, O[it]);
                     } else {
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) store4(static_cast<T*>(p.out) + at + 4 * ct, O[it][ct]);
+                        const u32x2 x = {pack_bf16x2(O[it][0], O[it][1]), pack_bf16x2(O[it][2], O[it][3])};
+                        poke_row(in_scalar(static_cast<T*>(p.out) + row), at * 2, x);
                     }
                 }
                 if constexpr (DOT != 0) {
                     if (tid < n) {
-                        float d = (s.dot[0][tid] + s.dot[1][tid]) + (s.dot[2][tid] + s.dot[3][tid]);
-                        if constexpr (DOT == 2)
-                            d += s.row[tid] - ((s.col[0][tid] + s.col[1][tid]) + (s.col[2][tid] + s.col[3][tid]));
+                        const auto four = [](const float* q) {
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(q);
+                            return (v[0] + v[1]) + (v[2] + v[3]);
+                        };
+                        float d = four(ra.gap(tid));
+                        if constexpr (W == 8) d += four(rb.gap(tid));
+                        if constexpr (DOT == 2) d += (rx.gap(tid)[0] + rx.gap(tid)[1]) - four(rc.gap(tid));
                         p.dots[h * p.tokens + t.row0 + t0 + tid] = d;
                     }
                 }
@@ -411,20 +412,21 @@ struct DecayBody {
             lds_barrier();   // everything of this chunk has been read
         }
 
+        // the state's addresses made anew: kept over the loop they would take a third of the registers
+        int lane2 = lane;
+        asm volatile("" : "+v"(lane2));
         float* sout = LOCAL ? p.local + (blk * p.H + h) * KV
                       : (p.seq_out && t.j == (REV ? 0 : t.nt - 1)) ? p.seq_out + (t.seq * p.H + h) * KV : nullptr;
         if (sout) {
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
+            for (int kt = 0; kt < KT; ++kt) {
+                if constexpr (TR) {
+                    *reinterpret_cast<f32x4*>(sout + state_at(w, lane2, kt, 0)) = S[kt];
+                } else {
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    if constexpr (TR) {
-                        *reinterpret_cast<f32x4*>(sout + state_at(w, lane, kt, ct, 0)) = S[kt][ct];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sout[state_at(w, lane, kt, ct, e)] = S[kt][ct][e];
-                    }
+                    for (int e = 0; e < 4; ++e) sout[state_at(w, lane2, kt, e)] = S[kt][e];
                 }
+            }
         }
         if (LOCAL && tid == 0) p.dec[blk * p.H + h] = total;
         if constexpr (DOT == 2) {      // <S', E> at the segment's end
@@ -433,24 +435,26 @@ struct DecayBody {
             float d = 0.f;
             if (e0) {
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
+                for (int kt = 0; kt < KT; ++kt) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane2, kt, 0));
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane, kt, ct, 0));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) d += v[e] * S[kt][ct][e];
-                    }
+                    for (int e = 0; e < 4; ++e) d += v[e] * S[kt][e];
+                }
             }
             d = wave_sum(d);
-            if (lane == 0) s.dot[w][0] = d;
+            if (lane == 0) s.ends[w] = d;
             __syncthreads();
-            if (tid == 0) p.ends[blk * p.H + h] = (s.dot[0][0] + s.dot[1][0]) + (s.dot[2][0] + s.dot[3][0]);
+            if (tid == 0) {
+                float all = 0.f;
+                for (int i = 0; i < W; ++i) all += s.ends[i];
+                p.ends[blk * p.H + h] = all;
+            }
         }
     }
 };
 
 template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(4 * DC, sizeof(T) == 2 ? DC / 32 : DC / 64) void decay_walk_kernel(DecayWalk p) {
     typedef DecayBody<T, DA, DC, REV, TR, DOT, LOCAL> B;
     __shared__ typename B::Shared s;
     B::run(p, s);
@@ -460,7 +464,7 @@ template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
 hipError_t launch_walk(const DecayWalk& p) {
     const int64_t blocks = (p.tiles + (LOCAL ? 0 : p.singles)) * p.H;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)blocks), dim3(256), 0,
+    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)blocks), dim3(4 * DC), 0,
                        p.stream, p);
     return hipGetLastError();
 }

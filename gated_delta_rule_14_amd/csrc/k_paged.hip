@@ -204,7 +204,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attn_
     constexpr int UR = R::UR, NV = 32 * UR / 64;     // 16-byte units of a row; units of a tile of V to a lane
     constexpr int DT = D / 16, KS = D / 32, NP = sizeof(T) == 2 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) union {
-        T v[4][32 * D];
+        T v[4][32 * Rows<T, D>::PITCH];
         float o[4][16 * D];
     } s;
     __shared__ float s_m[4][16], s_l[4][16];
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attn_
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int q = lane + 64 * i;
-            *reinterpret_cast<u32x4*>(vt.p + R::at(q / UR, q % UR)) = vf[i];
+            *reinterpret_cast<u32x4*>(vt.p + R::at(q / UR, q % UR * R::U)) = vf[i];
         }
         f32x4 S[2] = {zero4(), zero4()};
 #pragma unroll

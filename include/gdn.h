@@ -691,7 +691,8 @@ gdn_status gdn_short_conv_step(const gdn_conv_desc *d, const void *x, const floa
  * growing gates are followed as far as their products stay finite.
  *
  * Rows of q, k and v may lie in wider tensors: a token stride and a head stride
- * each (elements, multiples of 8; 0: dense).  Everything else is dense.
+ * each (elements, multiples of 8; 0: dense), a token's rows below 2^24 elements
+ * from the next one's.  Everything else is dense.
  */
 enum { GDN_DECAY_PER_HEAD = 1 };
 typedef struct gdn_decay_desc {
