@@ -19,8 +19,8 @@
 // R and C the row and column sums of the pairs (q_i k_j)(do_i v_j) e^{G_i-G_j},
 // j < i: sums of decayed terms only, so strong decays keep their digits.
 //
-// A workgroup walks the chunks of one segment of one head.  Each of its waves
-// owns 16 columns of c and S; S stays in MFMA accumulators, whose layout is that of an operand over its own rows, so S
+// A workgroup of four waves walks the chunks of one segment of one head.  Each
+// wave owns a quarter of the columns of c and S; S stays in MFMA accumulators, whose layout is that of an operand over its own rows, so S
 // never passes through LDS.  The pairs' products of the chunk are made once,
 // a tile row to a wave, and handed round in LDS.  Long sequences are cut into
 // segments: a first walk makes each segment's own state, launch_decay_join
@@ -122,7 +122,8 @@ template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
 struct DecayBody {
     typedef Eight<T> E8;
     typedef typename E8::frag frag;
-    static constexpr int W = DC / 16;         // waves: 16 columns each
+    static constexpr int CT = DC / 64;        // tiles of 16 columns of a wave
+    static constexpr int W = 4;               // waves
     static constexpr int KT = DA / 16;        // row tiles of S
     static constexpr int PW = 64 + 16 / sizeof(T);   // pitch of the pairs' rows
 
@@ -136,9 +137,11 @@ struct DecayBody {
         float ends[8];
     };
 
-    // offset of S tile kt's element e in the state's memory
-    __device__ __forceinline__ static int state_at(int w, int lane, int kt, int e) {
-        const int k = 32 * (kt >> 1) + 8 * (lane >> 4) + 4 * (kt & 1) + e, c = 16 * w + (lane & 15);
+    // offset of S tile (kt, ct)'s element e in the state's memory; the two tiles of a wave interleave
+    // by four columns, so that a lane's outputs are eight in a row
+    __device__ __forceinline__ static int state_at(int w, int lane, int kt, int ct, int e) {
+        const int g = lane >> 4, r = lane & 15, k = 32 * (kt >> 1) + 8 * g + 4 * (kt & 1) + e;
+        const int c = CT == 2 ? 32 * w + 8 * (r >> 2) + 4 * ct + (r & 3) : 16 * w + r;
         return TR ? c * DA + k : k * DC + c;
     }
 
@@ -190,22 +193,24 @@ struct DecayBody {
             return pg[at * p.gs];
         };
 
-        f32x4 S[KT];
+        f32x4 S[KT][CT];
         const float* sin = LOCAL ? nullptr
                            : single ? (p.seq_state ? p.seq_state + (t.seq * p.H + h) * KV : nullptr)
                                     : p.tile_state + (blk * p.H + h) * KV;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            S[kt] = zero4();
-            if (sin) {
-                if constexpr (TR) {
-                    S[kt] = *reinterpret_cast<const f32x4*>(sin + state_at(w, lane, kt, 0));
-                } else {
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) S[kt][e] = sin[state_at(w, lane, kt, e)];
+            for (int ct = 0; ct < CT; ++ct) {
+                S[kt][ct] = zero4();
+                if (sin) {
+                    if constexpr (TR) {
+                        S[kt][ct] = *reinterpret_cast<const f32x4*>(sin + state_at(w, lane, kt, ct, 0));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[kt][ct][e] = sin[state_at(w, lane, kt, ct, e)];
+                    }
                 }
             }
-        }
         float total = 1.f;   // LOCAL: decay of the segment
 
         constexpr int GW = REV ? W - 1 : 0;   // a wave with few or no pairs makes the gates
@@ -230,14 +235,12 @@ struct DecayBody {
                 if (j + 2 < nch) gnext = gate_of(j + 2);
             }
 
-            // ---- pairs: 16 rows and 64 (8 waves: 32) columns of a b^T to a wave, transposed in the
-            // accumulators (rows b's tokens); blocks of 32 columns beyond the diagonal are never read
+            // ---- pairs: 16 rows of a b^T to a wave, transposed in the accumulators (rows b's tokens);
+            // blocks of 32 columns beyond the diagonal are never read
             if constexpr (!LOCAL) {
-                constexpr int NJ = W == 8 ? 2 : 4;                     // tiles of a wave
-                const int it = W == 8 ? w >> 1 : w, j0 = W == 8 ? 2 * (w & 1) : 0;
-                const int i = 16 * it + r16;
+                const int it = w, i = 16 * it + r16;
                 float rsum = 0.f;
-                if (W == 4 || (REV ? j0 + 1 >= it : j0 <= it)) {
+                {
                     frag af[DA / 32], xf[DOT == 2 ? DC / 32 : 1];
 #pragma unroll
                     for (int q = 0; q < DA / 32; ++q) af[q] = ra.row8(i, 32 * q + 8 * g16);
@@ -247,8 +250,7 @@ struct DecayBody {
                     }
                     const float hi = gt.hi[i], lo = gt.lo[i];
 #pragma unroll
-                    for (int u = 0; u < NJ; ++u) {
-                        const int jt = j0 + u;
+                    for (int jt = 0; jt < 4; ++jt) {
                         if (REV ? (jt | 1) < it : (jt & ~1) > it) continue;
                         f32x4 P = zero4();
                         if (REV ? jt >= it : jt <= it) {
@@ -287,79 +289,100 @@ struct DecayBody {
                 }
                 if constexpr (DOT == 2) {
                     rsum = sum_groups(rsum);
-                    if (g16 == 0) rx.gap(i)[W == 8 ? w & 1 : 0] = rsum;
-                    if (W == 4 && g16 == 0) rx.gap(i)[1] = 0.f;
-                    if (it < 2 && (W == 4 || j0 == 2) && lane < 32) rc.gap(32 + lane)[it] = 0.f;   // no pairs of these rows
+                    if (g16 == 0) rx.gap(i)[0] = rsum;
+                    if (it < 2 && lane < 32) rc.gap(32 + lane)[it] = 0.f;   // no pairs of these rows
                 }
             }
 
             __builtin_amdgcn_sched_barrier(0);   // phases kept apart: fewer registers at once
             // ---- the state's part: O^T = S^T a^T, rows the wave's columns, columns the tokens
-            f32x4 O[4];
+            f32x4 O[4][CT];
             if constexpr (!LOCAL) {
                 constexpr int NP = DOT ? E8::PARTS : 1;
 #pragma unroll
-                for (int it = 0; it < 4; ++it) O[it] = zero4();
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) O[it][ct] = zero4();
 #pragma unroll
                 for (int q = 0; q < DA / 32; ++q) {
-                    frag sf[NP];
-                    float f[8];
+                    frag sf[CT][NP];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = S[2 * q + (e >> 2)][e & 3];
-                    E8::template split<NP>(f, sf);
+                    for (int ct = 0; ct < CT; ++ct) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = S[2 * q + (e >> 2)][ct][e & 3];
+                        E8::template split<NP>(f, sf[ct]);
+                    }
 #pragma unroll
                     for (int it = 0; it < 4; ++it) {
                         const frag b = ra.row8(16 * it + r16, 32 * q + 8 * g16);
 #pragma unroll
-                        for (int n = 0; n < NP; ++n) O[it] = E8::mma(sf[n], b, O[it]);
+                        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                            for (int n = 0; n < NP; ++n) O[it][ct] = E8::mma(sf[ct][n], b, O[it][ct]);
                     }
                 }
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     const int i = 16 * it + r16;
                     const float f = gt.in[i];
+                    float d = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) O[it][e] *= f;
+                    for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) O[it][ct][e] *= f;
+                        if constexpr (DOT != 0) {
+                            const f32x4 xv = rx.row4(i, 16 * CT * w + 4 * CT * g16 + 4 * ct);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) d += O[it][ct][e] * xv[e];
+                        }
+                    }
                     if constexpr (DOT != 0) {
-                        const f32x4 xv = rx.row4(i, 16 * w + 4 * g16);
-                        float d = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) d += O[it][e] * xv[e];
                         d = sum_groups(d);
-                        if (g16 == 0) (w < 4 ? ra : rb).gap(i)[w & 3] = d;
+                        if (g16 == 0) ra.gap(i)[w] = d;
                     }
                 }
             }
 
             __builtin_amdgcn_sched_barrier(0);
             // ---- the state: S <- dec S + b^T (out c)
-            frag cf[2];
+            frag cf[2][CT];
 #pragma unroll
-            for (int js = 0; js < 2; ++js) cf[js] = rc.template col8<false>(32 * js, 16 * w, lane);
+            for (int js = 0; js < 2; ++js)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    cf[js][ct] = rc.template col8<CT == 2>(32 * js, 16 * CT * w + 4 * ct, lane);
             const float dec = gt.dec;
             if (LOCAL) total *= dec;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[kt][e] *= dec;
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[kt][ct][e] *= dec;
 #pragma unroll
             for (int js = 0; js < 2; ++js) {
-                frag cp[E8::PARTS];
+                frag cp[CT][E8::PARTS];
                 const f32x4 wl = *reinterpret_cast<const f32x4*>(&gt.out[32 * js + 4 * g16]);
                 const f32x4 wh = *reinterpret_cast<const f32x4*>(&gt.out[32 * js + 16 + 4 * g16]);
-                float f[8];
-                E8::unpack(cf[js], f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[e] *= wl[e];
-                    f[4 + e] *= wh[e];
+                for (int ct = 0; ct < CT; ++ct) {
+                    float f[8];
+                    E8::unpack(cf[js][ct], f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[e] *= wl[e];
+                        f[4 + e] *= wh[e];
+                    }
+                    E8::template split<E8::PARTS>(f, cp[ct]);
                 }
-                E8::template split<E8::PARTS>(f, cp);
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
                     const frag b = rb.template col8<true>(32 * js, 32 * (kt >> 1) + 4 * (kt & 1), lane);
 #pragma unroll
-                    for (int n = 0; n < E8::PARTS; ++n) S[kt] = E8::mma(b, cp[n], S[kt]);
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int n = 0; n < E8::PARTS; ++n) S[kt][ct] = E8::mma(b, cp[ct][n], S[kt][ct]);
                 }
             }
 
@@ -378,22 +401,32 @@ struct DecayBody {
                             b = __builtin_shufflevector(reinterpret_cast<const f32x4*>(q)[0],
                                                         reinterpret_cast<const f32x4*>(q)[1], 0, 1, 2, 3, 4, 5, 6, 7);
                         }
-                        O[it] = E8::mma(cf[js], b, O[it]);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) O[it][ct] = E8::mma(cf[js][ct], b, O[it][ct]);
                     }
                 const int64_t t0 = first_of(j);
                 const int n = min(64, t.n - (int)t0);
                 const int64_t first = ((t.row0 + t0) * p.H + h) * DC;
-                unsigned at = (unsigned)r16 * (unsigned)(p.H * DC) + 16 * w + 4 * g16;
+                unsigned at = (unsigned)r16 * (unsigned)(p.H * DC) + 16 * CT * w + 4 * CT * g16;
                 asm volatile("" : "+v"(at));   // (a 64-bit form of it would be kept over the loop)
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     if (r16 >= n - 16 * it) continue;
                     const int64_t row = first + 16 * it * p.H * DC;
                     if (sizeof(T) == 4 || p.out32) {
-                        poke_row(in_scalar((p.out32 ? p.out32 : static_cast<float*>(p.out)) + row), at * 4, O[it]);
+                        float* q = in_scalar((p.out32 ? p.out32 : static_cast<float*>(p.out)) + row);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) poke_row(q, (at + 4 * ct) * 4, O[it][ct]);
                     } else {
-                        const u32x2 x = {pack_bf16x2(O[it][0], O[it][1]), pack_bf16x2(O[it][2], O[it][3])};
-                        poke_row(in_scalar(static_cast<T*>(p.out) + row), at * 2, x);
+                        unsigned x[2 * CT];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            x[2 * ct] = pack_bf16x2(O[it][ct][0], O[it][ct][1]);
+                            x[2 * ct + 1] = pack_bf16x2(O[it][ct][2], O[it][ct][3]);
+                        }
+                        T* q = in_scalar(static_cast<T*>(p.out) + row);
+                        if constexpr (CT == 2) poke_row(q, at * 2, u32x4{x[0], x[1], x[2], x[3]});
+                        else poke_row(q, at * 2, u32x2{x[0], x[1]});
                     }
                 }
                 if constexpr (DOT != 0) {
@@ -403,8 +436,7 @@ struct DecayBody {
                             return (v[0] + v[1]) + (v[2] + v[3]);
                         };
                         float d = four(ra.gap(tid));
-                        if constexpr (W == 8) d += four(rb.gap(tid));
-                        if constexpr (DOT == 2) d += (rx.gap(tid)[0] + rx.gap(tid)[1]) - four(rc.gap(tid));
+                        if constexpr (DOT == 2) d += rx.gap(tid)[0] - four(rc.gap(tid));
                         p.dots[h * p.tokens + t.row0 + t0 + tid] = d;
                     }
                 }
@@ -419,14 +451,16 @@ struct DecayBody {
                       : (p.seq_out && t.j == (REV ? 0 : t.nt - 1)) ? p.seq_out + (t.seq * p.H + h) * KV : nullptr;
         if (sout) {
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                if constexpr (TR) {
-                    *reinterpret_cast<f32x4*>(sout + state_at(w, lane2, kt, 0)) = S[kt];
-                } else {
+            for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sout[state_at(w, lane2, kt, e)] = S[kt][e];
+                for (int ct = 0; ct < CT; ++ct) {
+                    if constexpr (TR) {
+                        *reinterpret_cast<f32x4*>(sout + state_at(w, lane2, kt, ct, 0)) = S[kt][ct];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sout[state_at(w, lane2, kt, ct, e)] = S[kt][ct][e];
+                    }
                 }
-            }
         }
         if (LOCAL && tid == 0) p.dec[blk * p.H + h] = total;
         if constexpr (DOT == 2) {      // <S', E> at the segment's end
@@ -435,11 +469,13 @@ struct DecayBody {
             float d = 0.f;
             if (e0) {
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane2, kt, 0));
+                for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d += v[e] * S[kt][e];
-                }
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane2, kt, ct, 0));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d += v[e] * S[kt][ct][e];
+                    }
             }
             d = wave_sum(d);
             if (lane == 0) s.ends[w] = d;
@@ -454,7 +490,7 @@ struct DecayBody {
 };
 
 template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
-__global__ __launch_bounds__(4 * DC, sizeof(T) == 2 ? DC / 32 : DC / 64) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void decay_walk_kernel(DecayWalk p) {
     typedef DecayBody<T, DA, DC, REV, TR, DOT, LOCAL> B;
     __shared__ typename B::Shared s;
     B::run(p, s);
@@ -464,7 +500,7 @@ template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
 hipError_t launch_walk(const DecayWalk& p) {
     const int64_t blocks = (p.tiles + (LOCAL ? 0 : p.singles)) * p.H;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)blocks), dim3(4 * DC), 0,
+    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)blocks), dim3(256), 0,
                        p.stream, p);
     return hipGetLastError();
 }
