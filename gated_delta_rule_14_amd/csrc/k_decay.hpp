@@ -47,7 +47,9 @@ template <typename T, int D, int NT> struct Ahead {
     static constexpr int STEP = NT / R::UR, PER = 64 / STEP;     // rows between a thread's units
     u32x4 u[PER];
     __device__ __forceinline__ void load(const T* base, unsigned ts, int n, int tid) {
-        const unsigned tb = ts * sizeof(T), row = tid / R::UR * tb, unit = tid % R::UR * 16, last = (n - 1) * tb;
+        unsigned at = tid;
+        asm volatile("" : "+v"(at));   // (offsets made here are not kept over the loop)
+        const unsigned tb = ts * sizeof(T), row = at / R::UR * tb, unit = at % R::UR * 16, last = (n - 1) * tb;
         const T* p = in_scalar(base);
 #pragma unroll
         for (int i = 0; i < PER; ++i) u[i] = peek_row<u32x4>(p, min(row + STEP * i * tb, last) + unit);
@@ -213,7 +215,7 @@ struct DecayBody {
             }
         float total = 1.f;   // LOCAL: decay of the segment
 
-        constexpr int GW = REV ? W - 1 : 0;   // a wave with few or no pairs makes the gates
+        constexpr int GW = REV ? 1 : 2;   // a wave with one block of pairs makes the gates
         float gnext = 0.f;
         if (nch > 0) {
             fetch(0);
@@ -228,69 +230,74 @@ struct DecayBody {
             nc.put(rc, tid);
             if (DOT) nx.put(rx, tid);
             lds_barrier();
-            if (j + 1 < nch) fetch(j + 1);
             const ChunkGates& gt = s.gates[j & 1];
             if (w == GW && j + 1 < nch) {
                 make_gates<REV>(s.gates[(j + 1) & 1], gnext, t.n - first_of(j + 1), p.in_scale, p.up_scale, lane);
                 if (j + 2 < nch) gnext = gate_of(j + 2);
             }
 
-            // ---- pairs: 16 rows of a b^T to a wave, transposed in the accumulators (rows b's tokens);
-            // blocks of 32 columns beyond the diagonal are never read
+            // ---- pairs: blocks of 16 rows and 32 columns of a b^T, transposed in the accumulators
+            // (rows b's tokens), as the products read them.  Of the six that reach the diagonal or
+            // lie before it each wave has one of its own rows, and two waves another one.
+            int rr = r16, gg = g16;
+            asm volatile("" : "+v"(rr), "+v"(gg));   // (addresses made from these are not kept over the loop)
             if constexpr (!LOCAL) {
-                const int it = w, i = 16 * it + r16;
-                float rsum = 0.f;
-                {
-                    frag af[DA / 32], xf[DOT == 2 ? DC / 32 : 1];
+                const auto block = [&](int it, int js) {
+                    const int i = 16 * it + rr;
+                    f32x4 P[2] = {zero4(), zero4()};
 #pragma unroll
-                    for (int q = 0; q < DA / 32; ++q) af[q] = ra.row8(i, 32 * q + 8 * g16);
-                    if constexpr (DOT == 2) {
+                    for (int q = 0; q < DA / 32; ++q) {
+                        const frag af = ra.row8(i, 32 * q + 8 * gg);
 #pragma unroll
-                        for (int q = 0; q < DC / 32; ++q) xf[q] = rx.row8(i, 32 * q + 8 * g16);
+                        for (int u = 0; u < 2; ++u)
+                            P[u] = E8::mma(rb.row8(32 * js + 16 * u + rr, 32 * q + 8 * gg), af, P[u]);
                     }
                     const float hi = gt.hi[i], lo = gt.lo[i];
 #pragma unroll
-                    for (int jt = 0; jt < 4; ++jt) {
-                        if (REV ? (jt | 1) < it : (jt & ~1) > it) continue;
-                        f32x4 P = zero4();
-                        if (REV ? jt >= it : jt <= it) {
+                    for (int u = 0; u < 2; ++u) {
+                        const int j0 = 32 * js + 16 * u + 4 * gg;
+                        const f32x4 jh = *reinterpret_cast<const f32x4*>(&gt.hi[j0]);
+                        const f32x4 jl = *reinterpret_cast<const f32x4*>(&gt.lo[j0]);
 #pragma unroll
-                            for (int q = 0; q < DA / 32; ++q)
-                                P = E8::mma(rb.row8(16 * jt + r16, 32 * q + 8 * g16), af[q], P);
-                            const f32x4 jh = *reinterpret_cast<const f32x4*>(&gt.hi[16 * jt + 4 * g16]);
-                            const f32x4 jl = *reinterpret_cast<const f32x4*>(&gt.lo[16 * jt + 4 * g16]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = P[u][e] * (p.pair_scale * exp2_hw((hi - jh[e]) + (lo - jl[e])));
+                            P[u][e] = (REV ? j0 + e >= i : j0 + e <= i) ? y : 0.f;
+                        }
+                        store4(s.pairs + i * PW + 32 * js + 8 * gg + 4 * u, P[u]);
+                    }
+                    if constexpr (DOT == 2) {
+                        f32x4 M[2] = {zero4(), zero4()};
+#pragma unroll
+                        for (int q = 0; q < DC / 32; ++q) {
+                            const frag xf = rx.row8(i, 32 * q + 8 * gg);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                M[u] = E8::mma(rc.row8(32 * js + 16 * u + rr, 32 * q + 8 * gg), xf, M[u]);
+                        }
+                        float rsum = 0.f;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int j0 = 32 * js + 16 * u + 4 * gg;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int jj = 16 * jt + 4 * g16 + e;
-                                const float y = P[e] * (p.pair_scale * exp2_hw((hi - jh[e]) + (lo - jl[e])));
-                                P[e] = (REV ? jj >= i : jj <= i) ? y : 0.f;
+                                M[u][e] = j0 + e < i ? M[u][e] * P[u][e] : 0.f;
+                                rsum += M[u][e];
+                            }
+                            const f32x4 cs = row_sum16(M[u]);
+                            if (rr == 15) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) rc.gap(j0 + e)[it] = cs[e];
                             }
                         }
-                        if constexpr (DOT == 2) {
-                            f32x4 M = zero4();
-                            if (jt <= it) {
-#pragma unroll
-                                for (int q = 0; q < DC / 32; ++q)
-                                    M = E8::mma(rc.row8(16 * jt + r16, 32 * q + 8 * g16), xf[q], M);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    M[e] = 16 * jt + 4 * g16 + e < i ? M[e] * P[e] : 0.f;
-                                    rsum += M[e];
-                                }
-                            }
-                            const f32x4 cs = row_sum16(M);
-                            if (r16 == 15) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) rc.gap(16 * jt + 4 * g16 + e)[it] = cs[e];
-                            }
-                        }
-                        store4(s.pairs + i * PW + 32 * (jt >> 1) + 8 * g16 + 4 * (jt & 1), P);
+                        rsum = sum_groups(rsum);
+                        if (gg == 0) rx.gap(i)[js] = rsum;
                     }
-                }
+                };
+                block(w, REV ? 1 : 0);
+                if (REV ? w >= 2 : w < 2) block(3 - w, REV ? 0 : 1);
                 if constexpr (DOT == 2) {
-                    rsum = sum_groups(rsum);
-                    if (g16 == 0) rx.gap(i)[0] = rsum;
-                    if (it < 2 && lane < 32) rc.gap(32 + lane)[it] = 0.f;   // no pairs of these rows
+                    if (w < 2 && gg < 2) rc.gap(32 + 16 * gg + rr)[w] = 0.f;   // no pairs there
+                    if (w < 2 && gg == 0) rx.gap(16 * w + rr)[1] = 0.f;
                 }
             }
 
@@ -317,14 +324,14 @@ struct DecayBody {
                     for (int it = 0; it < 4; ++it) {
                         const frag b = ra.row8(16 * it + r16, 32 * q + 8 * g16);
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
+                        for (int n = 0; n < NP; ++n)
 #pragma unroll
-                            for (int n = 0; n < NP; ++n) O[it][ct] = E8::mma(sf[ct][n], b, O[it][ct]);
+                            for (int ct = 0; ct < CT; ++ct) O[it][ct] = E8::mma(sf[ct][n], b, O[it][ct]);
                     }
                 }
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
-                    const int i = 16 * it + r16;
+                    const int i = 16 * it + rr;
                     const float f = gt.in[i];
                     float d = 0.f;
 #pragma unroll
@@ -332,19 +339,21 @@ struct DecayBody {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) O[it][ct][e] *= f;
                         if constexpr (DOT != 0) {
-                            const f32x4 xv = rx.row4(i, 16 * CT * w + 4 * CT * g16 + 4 * ct);
+                            const f32x4 xv = rx.row4(i, 16 * CT * w + 4 * CT * gg + 4 * ct);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) d += O[it][ct][e] * xv[e];
                         }
                     }
                     if constexpr (DOT != 0) {
                         d = sum_groups(d);
-                        if (g16 == 0) ra.gap(i)[w] = d;
+                        if (gg == 0) ra.gap(i)[w] = d;
                     }
                 }
             }
 
             __builtin_amdgcn_sched_barrier(0);
+            // the next chunk's rows: not earlier, for their registers
+            if (j + 1 < nch) fetch(j + 1);
             // ---- the state: S <- dec S + b^T (out c)
             frag cf[2][CT];
 #pragma unroll
@@ -377,12 +386,16 @@ struct DecayBody {
                     E8::template split<E8::PARTS>(f, cp[ct]);
                 }
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const frag b = rb.template col8<true>(32 * js, 32 * (kt >> 1) + 4 * (kt & 1), lane);
+                for (int kt = 0; kt < KT; kt += 2) {
+                    frag b[2];
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
+                    for (int u = 0; u < 2; ++u) b[u] = rb.template col8<true>(32 * js, 16 * kt + 4 * u, lane);
 #pragma unroll
-                        for (int n = 0; n < E8::PARTS; ++n) S[kt][ct] = E8::mma(b, cp[ct][n], S[kt][ct]);
+                    for (int n = 0; n < E8::PARTS; ++n)      // (sums that do not wait for each other)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) S[kt + u][ct] = E8::mma(b[u], cp[ct][n], S[kt + u][ct]);
                 }
             }
 
@@ -436,7 +449,7 @@ struct DecayBody {
                             return (v[0] + v[1]) + (v[2] + v[3]);
                         };
                         float d = four(ra.gap(tid));
-                        if constexpr (DOT == 2) d += rx.gap(tid)[0] - four(rc.gap(tid));
+                        if constexpr (DOT == 2) d += (rx.gap(tid)[0] + rx.gap(tid)[1]) - four(rc.gap(tid));
                         p.dots[h * p.tokens + t.row0 + t0 + tid] = d;
                     }
                 }
