@@ -36,6 +36,7 @@ struct DecayWalk {
     float* dots = nullptr;        // [H][tokens]
     float *local = nullptr, *dec = nullptr;   // states of the segments alone [tiles][H][K][V], [tiles][H]
     int64_t H = 0, tokens = 0;
+    int share = 1;                // state heads to a head of q and k
     hipStream_t stream = nullptr;
 };
 // the walks of the forward, of its gradients and of a segment alone

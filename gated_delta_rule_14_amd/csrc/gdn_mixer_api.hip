@@ -92,7 +92,7 @@ DecayLayout decay_layout(const gdn_decay_desc* d, bool backward) {
 
 gdn_status check_decay_grid(const gdn_decay_desc* d, const DecayLayout& L) {
     const double H = (double)v_heads(d), per = (double)(d->key_dim * d->value_dim / 1024);
-    gdn_status s = check_grid(((double)L.tiles + (double)L.singles) * H, 256);
+    gdn_status s = check_grid(((double)L.tiles + (double)L.singles + 8) * H, 256);
     if (s == GDN_OK) s = check_grid((double)L.tiles * H * per, 256);
     // (the sums of dq and dk over shared heads: four elements to a thread)
     return s != GDN_OK ? s : check_grid((double)L.tokens * (double)(d->num_heads * d->key_dim / 4) / 256, 256);
@@ -123,6 +123,7 @@ gdn::DecayWalk walk_of(const gdn_decay_desc* d, const DecayLayout& L, const gdn:
     w.singles = L.singles;
     w.g = g;
     w.H = v_heads(d);
+    w.share = (int)(w.H / d->num_heads);
     w.gs = d->flags & GDN_DECAY_PER_HEAD ? 0 : w.H;
     w.tokens = L.tokens;
     w.stream = static_cast<hipStream_t>(stream);

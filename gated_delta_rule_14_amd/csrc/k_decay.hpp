@@ -142,14 +142,19 @@ struct DecayBody {
     // offset of S tile (kt, ct)'s element e in the state's memory; the two tiles of a wave interleave
     // by four columns, so that a lane's outputs are eight in a row
     __device__ __forceinline__ static int state_at(int w, int lane, int kt, int ct, int e) {
-        const int g = lane >> 4, r = lane & 15, k = 32 * (kt >> 1) + 8 * g + 4 * (kt & 1) + e;
+        const int g = lane >> 4, r = lane & 15, k = 16 * kt + 4 * g + e;
         const int c = CT == 2 ? 32 * w + 8 * (r >> 2) + 4 * ct + (r & 3) : 16 * w + r;
         return TR ? c * DA + k : k * DC + c;
     }
 
     __device__ static void run(const DecayWalk& p, Shared& s) {
         const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g16 = lane >> 4, r16 = lane & 15;
-        const int64_t blk = blockIdx.x / p.H, h = blockIdx.x - blk * p.H;
+        // workgroups go to the eight XCDs in turn: the heads that share q and k are put on one, next
+        // to each other, and read them through one L2
+        const unsigned xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, m = p.share, Hq = (unsigned)p.H / m;
+        const unsigned unit = slot / m * 8 + xcd;
+        const int64_t blk = unit / Hq, h = (unit - blk * Hq) * m + slot % m;
+        if (blk >= p.tiles + (LOCAL ? 0 : p.singles)) return;   // (the grid is a multiple of 8 heads)
         const bool single = blk >= p.tiles;
         Tile t;
         if (single && p.map.seqs) {
@@ -322,7 +327,7 @@ struct DecayBody {
                     }
 #pragma unroll
                     for (int it = 0; it < 4; ++it) {
-                        const frag b = ra.row8(16 * it + r16, 32 * q + 8 * g16);
+                        const frag b = ra.row44(16 * it + r16, 32 * q + 4 * g16);
 #pragma unroll
                         for (int n = 0; n < NP; ++n)
 #pragma unroll
@@ -389,7 +394,7 @@ struct DecayBody {
                 for (int kt = 0; kt < KT; kt += 2) {
                     frag b[2];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) b[u] = rb.template col8<true>(32 * js, 16 * kt + 4 * u, lane);
+                    for (int u = 0; u < 2; ++u) b[u] = rb.template col8<false>(32 * js, 16 * (kt + u), lane);
 #pragma unroll
                     for (int n = 0; n < E8::PARTS; ++n)      // (sums that do not wait for each other)
 #pragma unroll
@@ -511,10 +516,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void decay_walk_kernel
 
 template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
 hipError_t launch_walk(const DecayWalk& p) {
-    const int64_t blocks = (p.tiles + (LOCAL ? 0 : p.singles)) * p.H;
-    if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)blocks), dim3(256), 0,
-                       p.stream, p);
+    const int64_t units = (p.tiles + (LOCAL ? 0 : p.singles)) * (p.H / p.share);
+    if (units == 0) return hipSuccess;
+    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)((units + 7) / 8 * 8 * p.share)),
+                       dim3(256), 0, p.stream, p);
     return hipGetLastError();
 }
 
