@@ -39,9 +39,11 @@ struct DecayWalk {
     int share = 1;                // state heads to a head of q and k
     hipStream_t stream = nullptr;
 };
-// the walks of the forward, of its gradients and of a segment alone
-enum DecayKind { DECAY_O, DECAY_DQ, DECAY_DK, DECAY_DV, DECAY_LOCAL, DECAY_LOCAL_REV };
+// the walks of the forward, of its gradients and of a segment alone (for the forward)
+enum DecayKind { DECAY_O, DECAY_DQ, DECAY_DK, DECAY_DV, DECAY_LOCAL };
 hipError_t launch_decay_walk(const DecayWalk& w, DecayKind kind, int K, int V, bool bf16);
+// the segments alone for the gradients: f forward over (v, k), r from the end over (do, q)
+hipError_t launch_decay_local2(const DecayWalk& f, const DecayWalk& r, int K, int V, bool bf16);
 
 // Entering states of the segments out of their own, in place.
 struct DecayJoin {
@@ -54,7 +56,7 @@ struct DecayJoin {
     bool rev;                     // from the last segment to the first
     hipStream_t stream;
 };
-hipError_t launch_decay_join(const DecayJoin& a);
+hipError_t launch_decay_join(const DecayJoin& a, const DecayJoin* b = nullptr);   // b: another one of its sizes
 
 // dg out of the walks' dots: its running sum from each segment's end.
 struct DecayGate {

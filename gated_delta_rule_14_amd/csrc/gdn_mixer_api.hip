@@ -93,7 +93,7 @@ DecayLayout decay_layout(const gdn_decay_desc* d, bool backward) {
 gdn_status check_decay_grid(const gdn_decay_desc* d, const DecayLayout& L) {
     const double H = (double)v_heads(d), per = (double)(d->key_dim * d->value_dim / 1024);
     gdn_status s = check_grid(((double)L.tiles + (double)L.singles + 8) * H, 256);
-    if (s == GDN_OK) s = check_grid((double)L.tiles * H * per, 256);
+    if (s == GDN_OK) s = check_grid(2 * ((double)L.tiles + 8) * H * per, 256);
     // (the sums of dq and dk over shared heads: four elements to a thread)
     return s != GDN_OK ? s : check_grid((double)L.tokens * (double)(d->num_heads * d->key_dim / 4) / 256, 256);
 }
@@ -136,29 +136,27 @@ gdn_status walk(const gdn::DecayWalk& w, gdn::DecayKind kind, const gdn_decay_de
     return e == hipSuccess ? GDN_OK : hip_fail(e, "decay attention launch");
 }
 
-// The segments' own states (b, c) and their chaining from `first`.
-gdn_status segment_states(const gdn_decay_desc* d, const DecayLayout& L, gdn::DecayWalk w, const gdn::HeadRows& b,
-                          const gdn::HeadRows& c, float up, bool rev, const float* first, float* state, float* dec) {
-    if (L.tiles == 0) return GDN_OK;
+gdn::DecayWalk local_of(gdn::DecayWalk w, const gdn::HeadRows& b, const gdn::HeadRows& c, float up, float* state,
+                        float* dec) {
     w.b = b;
     w.c = c;
     w.up_scale = up;
     w.local = state;
     w.dec = dec;
-    const gdn_status s = walk(w, rev ? gdn::DECAY_LOCAL_REV : gdn::DECAY_LOCAL, d);
-    if (s != GDN_OK) return s;
+    return w;
+}
+gdn::DecayJoin join_of(const gdn_decay_desc* d, const gdn::DecayWalk& w, const float* first, bool rev) {
     gdn::DecayJoin j;
     j.map = w.map;
-    j.tiles = L.tiles;
-    j.state = state;
-    j.dec = dec;
+    j.tiles = w.tiles;
+    j.state = w.local;
+    j.dec = w.dec;
     j.first = first;
     j.H = w.H;
     j.KV = d->key_dim * d->value_dim;
     j.rev = rev;
     j.stream = w.stream;
-    const hipError_t e = gdn::launch_decay_join(j);
-    return e == hipSuccess ? GDN_OK : hip_fail(e, "decay attention state launch");
+    return j;
 }
 
 gdn_status check_decay_args(const gdn_decay_desc* d, const void* const* p16, int n, const float* g, const float* h0,
@@ -274,8 +272,12 @@ gdn_status gdn_decay_attn_fwd(const gdn_decay_desc* d, const void* q, const void
     const gdn::HeadRows K = rows_of(d, k, false, d->k_stride, d->k_head_stride);
     const gdn::HeadRows V = rows_of(d, v, true, d->v_stride, d->v_head_stride);
     float* state = reinterpret_cast<float*>(ws + L.state);
-    if ((s = segment_states(d, L, w, K, V, 1.f, false, h0, state, reinterpret_cast<float*>(ws + L.dec))) != GDN_OK)
-        return s;
+    if (L.tiles > 0) {
+        const gdn::DecayWalk f = local_of(w, K, V, 1.f, state, reinterpret_cast<float*>(ws + L.dec));
+        if ((s = walk(f, gdn::DECAY_LOCAL, d)) != GDN_OK) return s;
+        const hipError_t e = gdn::launch_decay_join(join_of(d, f, h0, false));
+        if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
+    }
     w.a = Q;
     w.b = K;
     w.c = V;
@@ -311,8 +313,14 @@ gdn_status gdn_decay_attn_bwd(const gdn_decay_desc* d, const void* q, const void
     const gdn::HeadRows K = rows_of(d, k, false, d->k_stride, d->k_head_stride);
     const gdn::HeadRows V = rows_of(d, v, true, d->v_stride, d->v_head_stride);
     const gdn::HeadRows O = rows_of(d, dout, true, 0, 0);
-    if ((s = segment_states(d, L, w0, K, V, 1.f, false, h0, at(L.state), at(L.dec))) != GDN_OK) return s;
-    if ((s = segment_states(d, L, w0, Q, O, d->scale, true, dht, at(L.estate), at(L.edec))) != GDN_OK) return s;
+    if (L.tiles > 0) {
+        const gdn::DecayWalk f = local_of(w0, V, K, 1.f, at(L.state), at(L.dec));
+        const gdn::DecayWalk r = local_of(w0, O, Q, d->scale, at(L.estate), at(L.edec));
+        hipError_t e = gdn::launch_decay_local2(f, r, (int)d->key_dim, (int)d->value_dim, d->dtype == GDN_DTYPE_BF16);
+        const gdn::DecayJoin jr = join_of(d, r, dht, true);
+        if (e == hipSuccess) e = gdn::launch_decay_join(join_of(d, f, h0, false), &jr);
+        if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
+    }
     const bool shared = v_heads(d) != d->num_heads;
 
     gdn::DecayWalk w = w0;          // dq: forward over (do, v, k)

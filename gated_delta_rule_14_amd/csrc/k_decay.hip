@@ -5,8 +5,31 @@
 
 namespace gdn {
 
-hipError_t launch_walk_local(const DecayWalk& p, int K, int V, bool bf, bool rev) {
-    return rev ? launch_walk_of<true, false, 0, true>(p, K, V, bf) : launch_walk_of<false, false, 0, true>(p, K, V, bf);
+// The segments' own states, forward (b, c) = (k, v) for the output; for the gradients
+// those of S^T, (v, k), and of E^T, (do, q) from the end, in one launch: each alone
+// leaves a fifth of the chip idle at its end.
+template <typename T, int DA, int DC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) void decay_local2_kernel(DecayWalk f, DecayWalk r, unsigned half) {
+    typedef DecayBody<T, DA, DC, false, true, 0, true> F;
+    typedef DecayBody<T, DA, DC, true, true, 0, true> R;
+    __shared__ typename F::Shared s;
+    static_assert(sizeof(typename F::Shared) == sizeof(typename R::Shared), "one layout");
+    if (blockIdx.x < half) F::run(f, blockIdx.x, s);
+    else R::run(r, blockIdx.x - half, reinterpret_cast<typename R::Shared&>(s));
+}
+template <typename T, int K, int V>
+static hipError_t local2(const DecayWalk& f, const DecayWalk& r) {
+    const unsigned half = walk_blocks(f, true);
+    if (half == 0) return hipSuccess;
+    hipLaunchKernelGGL((decay_local2_kernel<T, V, K>), dim3(2 * half), dim3(256), 0, f.stream, f, r, half);
+    return hipGetLastError();
+}
+hipError_t launch_decay_local2(const DecayWalk& f, const DecayWalk& r, int K, int V, bool bf) {
+    if (K == 64 && V == 64) return bf ? local2<bf16, 64, 64>(f, r) : local2<float, 64, 64>(f, r);
+    if (K == 64 && V == 128) return bf ? local2<bf16, 64, 128>(f, r) : local2<float, 64, 128>(f, r);
+    if (K == 128 && V == 64) return bf ? local2<bf16, 128, 64>(f, r) : local2<float, 128, 64>(f, r);
+    if (K == 128 && V == 128) return bf ? local2<bf16, 128, 128>(f, r) : local2<float, 128, 128>(f, r);
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_decay_walk(const DecayWalk& p, DecayKind kind, int K, int V, bool bf) {
@@ -15,18 +38,17 @@ hipError_t launch_decay_walk(const DecayWalk& p, DecayKind kind, int K, int V, b
         case DECAY_DQ: return launch_walk_dq(p, K, V, bf);
         case DECAY_DK: return launch_walk_dk(p, K, V, bf);
         case DECAY_DV: return launch_walk_dv(p, K, V, bf);
-        case DECAY_LOCAL: return launch_walk_local(p, K, V, bf, false);
-        case DECAY_LOCAL_REV: return launch_walk_local(p, K, V, bf, true);
+        case DECAY_LOCAL: return launch_walk_of<false, false, 0, true>(p, K, V, bf);
     }
     return hipErrorInvalidValue;
 }
 
 // S_0 = first, S_{j+1} = dec_j S_j + local_j over a sequence's segments; S_j takes
 // the place of local_j.  A workgroup takes 1024 elements of a sequence's state, by
-// the block of its first segment.
-__global__ __launch_bounds__(256) void decay_join_kernel(DecayJoin a) {
+// the block of its first segment; the next segment's are on their way meanwhile.
+__device__ __forceinline__ void join(const DecayJoin& a, unsigned block) {
     const int64_t per = (a.KV + 1023) / 1024, hb = a.H * per;
-    const int64_t c = blockIdx.x / hb, rest = blockIdx.x - c * hb, h = rest / per;
+    const int64_t c = block / hb, rest = block - c * hb, h = rest / per;
     const int64_t e = (rest - h * per) * 1024 + threadIdx.x * 4;
     const Tile t = tile_of(a.map, c);
     if (t.n == 0 || t.j != 0 || e >= a.KV) return;
@@ -47,17 +69,22 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecayJoin a) {
         }
     }
 }
+__global__ __launch_bounds__(256) void decay_join_kernel(DecayJoin a, DecayJoin b, unsigned half) {
+    if (blockIdx.x < half) join(a, blockIdx.x);
+    else join(b, blockIdx.x - half);
+}
 
-hipError_t launch_decay_join(const DecayJoin& a) {
-    const int64_t blocks = a.tiles * a.H * ((a.KV + 1023) / 1024);
-    if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)blocks), dim3(256), 0, a.stream, a);
+hipError_t launch_decay_join(const DecayJoin& a, const DecayJoin* b) {
+    const int64_t half = a.tiles * a.H * ((a.KV + 1023) / 1024);
+    if (half == 0) return hipSuccess;
+    hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)(b ? 2 * half : half)), dim3(256), 0, a.stream, a, b ? *b : a,
+                       (unsigned)half);
     return hipGetLastError();
 }
 
-// dg_t = <S, E> at the segment's end + the sum of the dots from t on, in 64 bits;
-// 0 where the gate lets nothing through.  A wave takes a segment of a head, 64
-// tokens at a time from its end.
+// dg_t = <S, E> at the segment's end + the sum of the dots from t on, carried in 64
+// bits from 64 tokens to the next; 0 where the gate lets nothing through.  A wave takes
+// a segment of a head from its end.
 __global__ __launch_bounds__(64) void decay_gate_kernel(DecayGate a) {
     const int lane = threadIdx.x;
     const int64_t blk = blockIdx.x / a.H, h = blockIdx.x - blk * a.H;
@@ -78,20 +105,17 @@ __global__ __launch_bounds__(64) void decay_gate_kernel(DecayGate a) {
     if (n == 0) return;
     double carry = a.ends[blk * a.H + h];
     const float *dq = a.dq + h * a.tokens + row0, *dk = a.dk + h * a.tokens + row0;
-    for (int t0 = (n - 1) & ~63; t0 >= 0; t0 -= 64) {
-        const int t = t0 + 63 - lane;     // lane 0 takes the last token
-        double x = t < n ? (double)dq[t] - (double)dk[t] : 0.0;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const double y = __shfl_up(x, off, 64);
-            if (lane >= off) x += y;
+    const float* g = a.g + row0 * a.gs + h;
+    int t = ((n - 1) & ~63) + 63 - lane;     // lane 0 takes the last token
+    float x = t < n ? dq[t] - dk[t] : 0.f, gt = t < n ? g[t * a.gs] : 0.f;
+    for (; t >= 0; t -= 64) {                // (alike in all lanes)
+        const float now = scan64(x), gn = gt;
+        if (t >= 64) {                       // the next ones are on their way
+            x = dq[t - 64] - dk[t - 64];
+            gt = g[(t - 64) * a.gs];
         }
-        x += carry;
-        if (t < n) {
-            const float g = a.g[(row0 + t) * a.gs + h];
-            a.dg[(row0 + t) * a.H + h] = gate_parts(g).hi == -8192.f ? 0.f : (float)x;
-        }
-        carry = __shfl(x, 63, 64);
+        if (t < n) a.dg[(row0 + t) * a.H + h] = gate_parts(gn).hi == -8192.f ? 0.f : (float)(carry + now);
+        carry += (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(now), 63));
     }
 }
 

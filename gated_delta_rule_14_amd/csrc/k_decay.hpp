@@ -147,11 +147,12 @@ struct DecayBody {
         return TR ? c * DA + k : k * DC + c;
     }
 
-    __device__ static void run(const DecayWalk& p, Shared& s) {
+    // block: the workgroup's number among those of this walk
+    __device__ static void run(const DecayWalk& p, unsigned block, Shared& s) {
         const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g16 = lane >> 4, r16 = lane & 15;
         // workgroups go to the eight XCDs in turn: the heads that share q and k are put on one, next
         // to each other, and read them through one L2
-        const unsigned xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, m = p.share, Hq = (unsigned)p.H / m;
+        const unsigned xcd = block & 7, slot = block >> 3, m = p.share, Hq = (unsigned)p.H / m;
         const unsigned unit = slot / m * 8 + xcd;
         const int64_t blk = unit / Hq, h = (unit - blk * Hq) * m + slot % m;
         if (blk >= p.tiles + (LOCAL ? 0 : p.singles)) return;   // (the grid is a multiple of 8 heads)
@@ -508,18 +509,24 @@ struct DecayBody {
 };
 
 template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? (LOCAL ? 3 : 2) : 1) void decay_walk_kernel(DecayWalk p) {
     typedef DecayBody<T, DA, DC, REV, TR, DOT, LOCAL> B;
     __shared__ typename B::Shared s;
-    B::run(p, s);
+    B::run(p, blockIdx.x, s);
+}
+
+// workgroups of a walk, a multiple of 8 heads' (see run)
+inline unsigned walk_blocks(const DecayWalk& p, bool local) {
+    const int64_t units = (p.tiles + (local ? 0 : p.singles)) * (p.H / p.share);
+    return (unsigned)((units + 7) / 8 * 8 * p.share);
 }
 
 template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
 hipError_t launch_walk(const DecayWalk& p) {
-    const int64_t units = (p.tiles + (LOCAL ? 0 : p.singles)) * (p.H / p.share);
-    if (units == 0) return hipSuccess;
-    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3((unsigned)((units + 7) / 8 * 8 * p.share)),
-                       dim3(256), 0, p.stream, p);
+    const unsigned blocks = walk_blocks(p, LOCAL);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3(blocks), dim3(256), 0,
+                       p.stream, p);
     return hipGetLastError();
 }
 
@@ -541,6 +548,5 @@ hipError_t launch_walk_o(const DecayWalk& p, int K, int V, bool bf);
 hipError_t launch_walk_dq(const DecayWalk& p, int K, int V, bool bf);
 hipError_t launch_walk_dk(const DecayWalk& p, int K, int V, bool bf);
 hipError_t launch_walk_dv(const DecayWalk& p, int K, int V, bool bf);
-hipError_t launch_walk_local(const DecayWalk& p, int K, int V, bool bf, bool rev);
 
 }  // namespace gdn
