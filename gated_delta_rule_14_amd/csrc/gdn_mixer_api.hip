@@ -181,8 +181,8 @@ gdn_status check_pages(const gdn_pages* c, int64_t heads, int64_t D, const void*
     if (!c) return api_fail(GDN_ERR_NULL_ARG, "pages is NULL");
     const int64_t lim = (int64_t)1 << 31;
     if (c->num_seqs < 0 || c->max_pages <= 0 || c->pages <= 0 || c->page_size <= 0 || c->num_seqs >= lim ||
-        c->pages >= lim || c->max_pages >= lim || c->page_size >= lim || c->max_pages * c->page_size >= lim)
-        return api_fail(GDN_ERR_BAD_SHAPE, "N=%lld max_pages=%lld pages=%lld page_size=%lld (a table row below 2^31 tokens)",
+        c->pages >= lim || c->max_pages >= lim || c->page_size >= lim || c->max_pages * c->page_size >= lim / 2)
+        return api_fail(GDN_ERR_BAD_SHAPE, "N=%lld max_pages=%lld pages=%lld page_size=%lld (a table row below 2^30 tokens)",
                         (long long)c->num_seqs, (long long)c->max_pages, (long long)c->pages, (long long)c->page_size);
     const int64_t st[2][3] = {{c->k_page_stride, c->k_token_stride, c->k_head_stride},
                               {c->v_page_stride, c->v_token_stride, c->v_head_stride}};

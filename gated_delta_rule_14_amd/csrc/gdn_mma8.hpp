@@ -126,6 +126,21 @@ template <typename T, int D> struct Rows {
             return v;
         }
     }
+    // The same with 16 rows: rows 4g + 0..3, and zeros.
+    __device__ __forceinline__ frag col4(int d0, int lane) const {
+        const int g = lane >> 4, r = lane & 15;
+        if constexpr (sizeof(T) == 2) {
+            typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + at(4 * g + (r >> 2), d0 + 4 * (r & 3))));
+            const u32x2 x = __builtin_bit_cast(u32x2, lo);
+            return __builtin_bit_cast(frag, u32x4{x.x, x.y, 0, 0});
+        } else {
+            frag v;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < 4 ? p[at(4 * g + e, d0 + r)] : 0.f;
+            return v;
+        }
+    }
 };
 
 }  // namespace gdn

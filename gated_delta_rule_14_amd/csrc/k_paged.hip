@@ -17,7 +17,7 @@ namespace gdn {
 template <typename A>
 __device__ __forceinline__ int2 slot_of(const A& a, int64_t n, int64_t pos) {
     if (pos < 0 || pos >= a.M * a.page) return make_int2(-1, 0);
-    const unsigned pg = (unsigned)pos / (unsigned)a.page;    // M * page is below 2^31
+    const unsigned pg = (unsigned)pos / (unsigned)a.page;    // M * page is below 2^30
     const int id = a.table[n * a.M + pg];
     return make_int2((unsigned)id < (unsigned)a.pages ? id : -1, (int)((unsigned)pos - pg * (unsigned)a.page));
 }
@@ -121,14 +121,15 @@ hipError_t launch_paged_append(const PagedAppend& a) {
 // sequences together make about `share` pieces whatever their lengths; a
 // workgroup takes a piece for one key head and up to 16 of the query heads that
 // share it, and a second launch joins the pieces of the sequences that have
-// several.  Its four waves take 32 tokens in turn, each with a maximum, sum and
-// output of its own, and meet at the end.
+// several.  Its four waves take 32 tokens in turn (16 of heads wider than 128, so that
+// keys and values on their way and the output fit the registers of two workgroups to a
+// compute unit), each with a maximum, sum and output of its own, and meet at the end.
 //
 // Scores are K Q^T, tokens in the accumulator's rows, so they are at once the
 // operand of the output's product V^T P^T, whose V^T comes out of LDS by
 // transposing reads.  With bf16 the weights go into that product in two parts,
 // 16 bits.
-constexpr int UNIT = 128;       // tokens that the four waves take in a turn
+constexpr int UNIT = 128;       // tokens that a piece is a multiple of
 
 struct Piece {
     int64_t n;                  // sequence; < 0: none
@@ -146,29 +147,27 @@ __device__ __forceinline__ void range_of(const PagedAttn& a, int64_t n, int* lo,
 }
 __device__ __forceinline__ int units_of(int lo, int len) { return (len - (lo & ~31) + UNIT - 1) / UNIT; }
 
-// Units of a piece, from the sum over the sequences; the whole wave calls it.
-__device__ __forceinline__ int piece_units(const PagedAttn& a, int lane) {
-    int64_t all = 0;
-    for (int64_t b = 0; b < a.N; b += 64) {
+// Piece number `at` (of sequence `seq` if that is not negative: its first one); the whole
+// wave calls it.  A piece has as many units as the sum over the sequences asks for.
+__device__ __forceinline__ Piece find_piece(const PagedAttn& a, int64_t at, int64_t seq, int lane) {
+    int lo0 = 0, len0 = 0;                        // the first 64 sequences' stay in registers
+    if (lane < a.N) range_of(a, lane, &lo0, &len0);
+    int64_t all = units_of(lo0, len0);
+    for (int64_t b = 64; b < a.N; b += 64) {
         int lo = 0, len = 0;
         if (b + lane < a.N) range_of(a, b + lane, &lo, &len);
         all += units_of(lo, len);
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off, 64);
-    return (int)max((int64_t)1, (all + a.share - 1) / a.share);
-}
-
-// Piece number `at` (of sequence `seq` if that is not negative: its first one).
-__device__ __forceinline__ Piece find_piece(const PagedAttn& a, int64_t at, int64_t seq, int lane) {
-    const int per = piece_units(a, lane);
+    const int per = (int)max((int64_t)1, (all + a.share - 1) / a.share);
     Piece p;
     p.n = -1;
     int64_t before = 0;
     for (int64_t b = 0; b < a.N; b += 64) {
-        int lo = 0, len = 0, cnt = 0;
+        int lo = lo0, len = len0, cnt = 0;
         if (b + lane < a.N) {
-            range_of(a, b + lane, &lo, &len);
+            if (b > 0) range_of(a, b + lane, &lo, &len);
             cnt = max(1, (units_of(lo, len) + per - 1) / per);
         }
         int inc = cnt;
@@ -197,14 +196,15 @@ __device__ __forceinline__ Piece find_piece(const PagedAttn& a, int64_t at, int6
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attn_kernel(PagedAttn a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(PagedAttn a) {
     typedef Eight<T> E8;
     typedef typename E8::frag frag;
     typedef Rows<T, D> R;
-    constexpr int UR = R::UR, NV = 32 * UR / 64;     // 16-byte units of a row; units of a tile of V to a lane
+    constexpr int TT = D <= 128 ? 32 : 16, TH = TT / 16, TURN = 4 * TT;   // tokens of a wave and of the four in a turn
+    constexpr int UR = R::UR, NV = TT * UR / 64;     // 16-byte units of a row; units of a tile of V to a lane
     constexpr int DT = D / 16, KS = D / 32, NP = sizeof(T) == 2 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) union {
-        T v[4][32 * Rows<T, D>::PITCH];
+        T v[4][TT * Rows<T, D>::PITCH];
         float o[4][16 * D];
     } s;
     __shared__ float s_m[4][16], s_l[4][16];
@@ -233,17 +233,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attn_
     }
 
     const R vt{s.v[w]};
-    frag kf[2][KS];
+    frag kf[TH][KS];
     u32x4 vf[NV];
     unsigned seen = 0;
-    // keys and values of tokens t0 .. t0 + 31 that are seen; zeros for the others
-    const auto fetch = [&](int t0) {
-        const int t = t0 + (lane & 31);
-        const int2 at = slot_of(a, n, t >= pc.lo && t < pc.last ? t : -1);
+    // the page and slot of token t0 + lane % TT, if it is seen
+    const auto look = [&](int t0) {
+        const int t = t0 + (lane & (TT - 1));
+        return slot_of(a, n, t >= pc.lo && t < pc.last ? t : -1);
+    };
+    // keys and values of TT tokens that are seen; zeros for the others
+    const auto fetch = [&](int2 at) {
         seen = (unsigned)__ballot(at.x >= 0);
         const int64_t ko = at.x * a.kc.ps + at.y * a.kc.ts, vo = at.x * a.vc.ps + at.y * a.vc.ts;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < TH; ++h) {
             const T* p = kc + __shfl(ko, 16 * h + r, 64) + 8 * g;
 #pragma unroll
             for (int q = 0; q < KS; ++q) {
@@ -275,33 +278,45 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attn_
 #pragma unroll
     for (int i = 0; i < DT; ++i) O[i] = zero4();
     float mx = -INFINITY, sum = 0.f;
-    int t0 = pc.first + 32 * w;
-    if (t0 < pc.last) fetch(t0);
-    for (; t0 < pc.last; t0 += UNIT) {
+    int t0 = pc.first + TT * w;
+    int2 next = make_int2(-1, 0);
+    if (t0 < pc.last) {
+        fetch(look(t0));
+        next = look(t0 + TURN);        // (a turn ahead: the table's latency is not waited for)
+    }
+    for (; t0 < pc.last; t0 += TURN) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int q = lane + 64 * i;
             *reinterpret_cast<u32x4*>(vt.p + R::at(q / UR, q % UR * R::U)) = vf[i];
         }
-        f32x4 S[2] = {zero4(), zero4()};
+        f32x4 S[TH];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < TH; ++h) {
+            S[h] = zero4();
 #pragma unroll
             for (int q = 0; q < KS; ++q) S[h] = E8::mma(kf[h][q], qf[q], S[h]);
+        }
         const unsigned in = seen;
-        if (t0 + UNIT < pc.last) fetch(t0 + UNIT);
+        if (t0 + TURN < pc.last) {
+            fetch(next);
+            next = look(t0 + 2 * TURN);
+        }
         float x[8], top = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int t = 16 * (e >> 2) + 4 * g + (e & 3);
-            x[e] = in >> t & 1 ? S[e >> 2][e & 3] * a.scale : -INFINITY;
-            top = fmaxf(top, x[e]);
+            x[e] = -INFINITY;
+            if (e < 4 * TH) {
+                const int t = 16 * (e >> 2) + 4 * g + (e & 3);
+                if (in >> t & 1) x[e] = S[(e >> 2) % TH][e & 3] * a.scale;
+                top = fmaxf(top, x[e]);
+            }
         }
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float next = fmaxf(mx, top), ref = next == -INFINITY ? 0.f : next;
+        const float m1 = fmaxf(mx, top), ref = m1 == -INFINITY ? 0.f : m1;
         const float keep = exp2_hw(mx - ref);
-        mx = next;
+        mx = m1;
         float l = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -315,7 +330,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void attn_
         for (int i = 0; i < DT; ++i) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) O[i][e] *= keep;
-            const frag v = vt.template col8<false>(0, 16 * i, lane);
+            const frag v = TT == 32 ? vt.template col8<false>(0, 16 * i, lane) : vt.col4(16 * i, lane);
 #pragma unroll
             for (int k = 0; k < NP; ++k) O[i] = E8::mma(v, pf[k], O[i]);
         }

@@ -762,7 +762,7 @@ gdn_status gdn_decay_attn_step(const gdn_decay_desc *d, const void *q, const voi
  */
 typedef struct gdn_pages {
     int64_t num_seqs;       /* N: rows of page_table */
-    int64_t max_pages;      /* entries of a row; max_pages * page_size below 2^31 */
+    int64_t max_pages;      /* entries of a row; max_pages * page_size below 2^30 */
     int64_t pages;          /* of the pool */
     int64_t page_size;      /* tokens of a page, >= 1 */
     int64_t k_page_stride, k_token_stride, k_head_stride;
