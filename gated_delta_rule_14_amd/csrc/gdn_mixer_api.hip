@@ -235,7 +235,7 @@ gdn_status check_attn(const gdn_paged_attn_desc* d) {
                         (long long)d->q_head_stride);
     if (h % 8 || d->q_stride % 8) return api_fail(GDN_ERR_MISALIGNED, "strides must be multiples of 8 elements");
     const double N = (double)d->num_seqs;
-    const gdn_status s = check_grid((N + 1024) * (double)d->k_heads * (double)((d->q_heads / d->k_heads + 15) / 16), 256);
+    const gdn_status s = check_grid((N + 2048) * (double)d->k_heads * (double)((d->q_heads / d->k_heads + 15) / 16), 256);
     return s != GDN_OK ? s : check_grid(N * (double)d->q_heads, 256);
 }
 size_t attn_rows(const gdn_paged_attn_desc* d) {
