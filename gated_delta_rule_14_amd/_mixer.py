@@ -67,6 +67,11 @@ def _decay_plan(B, T, H, HV, K, V, N, qs, ks, vs, qh, kh, vh, code, flags, scale
     return p
 
 
+@lru_cache(maxsize=1024)
+def _step_plan(*fields):
+    return _Plan(DecayDesc(*fields))
+
+
 def _decay(q, k, v, g, scale, packed):
     """Checks shared by the entry points (tensors [B, T, heads, width]): the plan and the device."""
     dev, qs, vs = _device(q, "q"), q.shape, v.shape
@@ -146,28 +151,37 @@ def decay_attn_bwd(q, k, v, g, do, scale=None, h0=None, dht=None, cu_seqlens=Non
     return out
 
 
+def _rows(t, name):
+    """(stride, head stride) of t [N, H, W]; (0, 0) when dense."""
+    return (0, 0) if t.is_contiguous() else _heads(t[:, None], name)
+
+
 def decay_attn_step(q, k, v, g, state, scale=None, o=None, stream=None):
     """gdn_decay_attn_step: one token of N sequences, q, k [N, H, K] and v [N,
     H_V, V]; g [N, H_V] or [H_V]; state [N, H_V, K, V] float32 is updated in
     place.  Returns o [N, H_V, V]."""
     lib = _b.load()
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k must be [N, H, K] and v [N, H_V, V]")
-    dev = _device(q, "q")
-    p, dev = _decay(q[:, None], k[:, None], v[:, None], g if g.dim() == 1 else g[:, None], scale, 0) \
-        if q.shape[0] else (None, dev)
-    sh = v.shape
+    dev, qs, vs = _device(q, "q"), q.shape, v.shape
+    if len(qs) != 3 or k.shape != qs or len(vs) != 3 or vs[0] != qs[0]:
+        raise ValueError("q, k [N, H, K] and v [N, H_V, V] do not match: %s, %s, %s" % (tuple(qs), tuple(k.shape), tuple(vs)))
+    if k.dtype != q.dtype or v.dtype != q.dtype or k.device != dev or v.device != dev:
+        raise ValueError("k and v must have the type and device of q")
     if state is None:
         raise ValueError("state is required")
-    _dense(state, "state", (sh[0], sh[1], q.shape[2], sh[2]), dev)
+    N, H, K = qs
+    HV, V = vs[1], vs[2]
+    _dense(state, "state", (N, HV, K, V), dev)
+    flags = DECAY_PER_HEAD if g.dim() == 1 else 0
+    _dense(g, "g", (HV,) if flags else (N, HV), dev)
     if o is not None:
-        _dense(o, "o", sh, dev, q.dtype)
+        _dense(o, "o", vs, dev, q.dtype)
     else:
         with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
             o = _like(v)
-    if p is not None:
-        _run(lib.gdn_decay_attn_step, dev, stream, p.at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-             state.data_ptr(), o.data_ptr())
+    (qt, qh), (kt, kh), (vt, vh) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    p = _step_plan(N, 1, H, HV, K, V, 0, qt, kt, vt, qh, kh, vh, _code(q, "q"), flags, K ** -0.5 if scale is None else float(scale))
+    _run(lib.gdn_decay_attn_step, dev, stream, p.at, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+         state.data_ptr(), o.data_ptr())
     return o
 
 
@@ -210,13 +224,14 @@ def _pages(k_cache, v_cache, page_table, lens, like, heads, D, dev):
     return _pages_plan(N, M, sh[0], sh[1], *k_cache.stride()[:3], *v_cache.stride()[:3]), N
 
 
-def _look(k_cache, page_table, lens, news, stream, dev):
-    """With GDN_DEBUG set: raise where a position in use has no page.  `news`: tokens after lens."""
+def _look(k_cache, page_table, lens, T, cu_seqlens, stream, dev):
+    """With GDN_DEBUG set: raise where a position in use has no page, T tokens (or a packed
+    sequence's) after lens."""
     if not _debug():
         return
     (stream or torch.cuda.current_stream(dev)).synchronize()
     table, n = page_table.cpu(), lens.cpu()
-    end = n + news
+    end = n + (T if cu_seqlens is None else (cu_seqlens[1:] - cu_seqlens[:-1]).cpu())
     cap = table.shape[1] * k_cache.shape[1]
     if bool(((n < 0) | (end > cap)).any()):
         raise ValueError("lens must be in 0 .. %d with the new tokens" % cap)
@@ -275,9 +290,7 @@ def paged_append(q, k, v, k_cache, v_cache, page_table, lens, inv_freq=None, pos
     else:
         with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
             q_out = _like(q)
-    if _debug():
-        news = T if not packed else (cu_seqlens[1:] - cu_seqlens[:-1]).cpu()
-        _look(k_cache, page_table, lens, news, stream, dev)
+    _look(k_cache, page_table, lens, T, cu_seqlens, stream, dev)
     _run(lib.gdn_paged_append, dev, stream, p.at, c.at, _p(q), k.data_ptr(), v.data_ptr(), vt, vh, _p(q_weight),
          _p(k_weight), _p(inv_freq), _p(positions), _p(cu_seqlens), page_table.data_ptr(), lens.data_ptr(), _p(q_out),
          k_cache.data_ptr(), v_cache.data_ptr())
@@ -321,7 +334,7 @@ def paged_attn(q, k_cache, v_cache, page_table, lens, scale=None, window=0, o=No
         if o is None:
             o = _like(q)
         workspace, have = _workspace(workspace, p.fwd, dev, q)
-    _look(k_cache, page_table, lens, 0, stream, dev)
+    _look(k_cache, page_table, lens, 0, None, stream, dev)
     _run(lib.gdn_paged_attn, dev, stream, p.at, c.at, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
          page_table.data_ptr(), lens.data_ptr(), o.data_ptr(), _p(workspace), have)
     return o
