@@ -53,6 +53,8 @@ struct DecayJoin {
     const float* dec;             // [tiles][H]
     const float* first;           // [N][H][K][V] or nullptr
     int64_t H, KV;
+    int V;                        // with own_order the states' elements are in the forward walk's
+    bool own_order;               //   order, but those of `first`, which are [K][V]
     bool rev;                     // from the last segment to the first
     hipStream_t stream;
 };

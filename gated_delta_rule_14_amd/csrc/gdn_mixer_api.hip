@@ -148,8 +148,11 @@ gdn::DecayWalk local_of(gdn::DecayWalk w, const gdn::HeadRows& b, const gdn::Hea
     w.dec = dec;
     return w;
 }
-gdn::DecayJoin join_of(const gdn_decay_desc* d, const gdn::DecayWalk& w, const float* first, bool rev) {
+gdn::DecayJoin join_of(const gdn_decay_desc* d, const gdn::DecayWalk& w, const float* first, bool rev,
+                       bool own_order) {
     gdn::DecayJoin j;
+    j.V = (int)d->value_dim;
+    j.own_order = own_order;
     j.map = w.map;
     j.tiles = w.tiles;
     j.state = w.local;
@@ -278,7 +281,7 @@ gdn_status gdn_decay_attn_fwd(const gdn_decay_desc* d, const void* q, const void
     if (L.tiles > 0) {
         const gdn::DecayWalk f = local_of(w, K, V, 1.f, state, reinterpret_cast<float*>(ws + L.dec));
         if ((s = walk(f, gdn::DECAY_LOCAL, d)) != GDN_OK) return s;
-        const hipError_t e = gdn::launch_decay_join(join_of(d, f, h0, false));
+        const hipError_t e = gdn::launch_decay_join(join_of(d, f, h0, false, true));
         if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
     }
     w.a = Q;
@@ -320,8 +323,8 @@ gdn_status gdn_decay_attn_bwd(const gdn_decay_desc* d, const void* q, const void
         const gdn::DecayWalk f = local_of(w0, V, K, 1.f, at(L.state), at(L.dec));
         const gdn::DecayWalk r = local_of(w0, O, Q, d->scale, at(L.estate), at(L.edec));
         hipError_t e = gdn::launch_decay_local2(f, r, (int)d->key_dim, (int)d->value_dim, d->dtype == GDN_DTYPE_BF16);
-        const gdn::DecayJoin jr = join_of(d, r, dht, true);
-        if (e == hipSuccess) e = gdn::launch_decay_join(join_of(d, f, h0, false), &jr);
+        const gdn::DecayJoin jr = join_of(d, r, dht, true, false);
+        if (e == hipSuccess) e = gdn::launch_decay_join(join_of(d, f, h0, false, false), &jr);
         if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
     }
     const bool shared = v_heads(d) != d->num_heads;

@@ -53,7 +53,18 @@ __device__ __forceinline__ void join(const DecayJoin& a, unsigned block) {
     const Tile t = tile_of(a.map, c);
     if (t.n == 0 || t.j != 0 || e >= a.KV) return;
     f32x4 s = zero4();
-    if (a.first) s = *reinterpret_cast<const f32x4*>(a.first + (t.seq * a.H + h) * a.KV + e);
+    if (a.first) {
+        const float* first = a.first + (t.seq * a.H + h) * a.KV;
+        if (a.own_order) {                 // element e in the walk's order (DecayBody::own_at, state_at)
+            const int ct2 = a.V == 128, i = (int)e >> 2, lane = i & 63, w = i >> 6 & 3, tile = i >> 8;
+            const int kt = tile >> ct2, ct = tile & ct2, r = lane & 15;
+            const int k = 16 * kt + 4 * (lane >> 4), c = ct2 ? 32 * w + 8 * (r >> 2) + 4 * ct + (r & 3) : 16 * w + r;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[x] = first[(k + x) * a.V + c];
+        } else {
+            s = *reinterpret_cast<const f32x4*>(first + e);
+        }
+    }
     const int64_t step = a.rev ? -1 : 1;
     int64_t at = c + (a.rev ? t.nt - 1 : 0);
     f32x4 next = *reinterpret_cast<const f32x4*>(a.state + (at * a.H + h) * a.KV + e);
