@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.hip", "k_step.hip", "k_table.hip", "k_intra.hip", "k_scan.hip", "k_bwd.hip",
            "k_bwd_kda.hip", "k_fused.hip", "gdn_layer_api.hip", "k_tiles.hip", "k_linrec.hip",
            "k_qknorm.hip", "k_conv.hip", "gdn_mixer_api.hip", "k_decay.hip", "k_decay_o.hip",
-           "k_decay_dq.hip", "k_decay_dk.hip", "k_decay_dv.hip", "k_paged.hip"]
+           "k_decay_grad.hip", "k_paged.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -39,9 +39,10 @@ struct DecayWalk {
     int share = 1;                // state heads to a head of q and k
     hipStream_t stream = nullptr;
 };
-// the walks of the forward, of its gradients and of a segment alone (for the forward)
-enum DecayKind { DECAY_O, DECAY_DQ, DECAY_DK, DECAY_DV, DECAY_LOCAL };
-hipError_t launch_decay_walk(const DecayWalk& w, DecayKind kind, int K, int V, bool bf16);
+// the forward: the output, or (local) the segments' own states
+hipError_t launch_decay_walk(const DecayWalk& w, bool local, int K, int V, bool bf16);
+// dq, dk and dv, walks of one map
+hipError_t launch_decay_grad(const DecayWalk& q, const DecayWalk& k, const DecayWalk& v, int K, int V, bool bf16);
 // the segments alone for the gradients: f forward over (v, k), r from the end over (do, q)
 hipError_t launch_decay_local2(const DecayWalk& f, const DecayWalk& r, int K, int V, bool bf16);
 

@@ -96,7 +96,7 @@ DecayLayout decay_layout(const gdn_decay_desc* d, bool backward) {
 
 gdn_status check_decay_grid(const gdn_decay_desc* d, const DecayLayout& L) {
     const double H = (double)v_heads(d), per = (double)(d->key_dim * d->value_dim / 1024);
-    gdn_status s = check_grid(((double)L.tiles + (double)L.singles + 8) * H, 256);
+    gdn_status s = check_grid(3 * ((double)L.tiles + (double)L.singles + 8) * H, 256);
     if (s == GDN_OK) s = check_grid(2 * ((double)L.tiles + 8) * H * per, 256);
     // (the sums of dq and dk over shared heads: four elements to a thread)
     return s != GDN_OK ? s : check_grid((double)L.tokens * (double)(d->num_heads * d->key_dim / 4) / 256, 256);
@@ -134,9 +134,9 @@ gdn::DecayWalk walk_of(const gdn_decay_desc* d, const DecayLayout& L, const gdn:
     return w;
 }
 
-gdn_status walk(const gdn::DecayWalk& w, gdn::DecayKind kind, const gdn_decay_desc* d) {
+gdn_status walk(const gdn::DecayWalk& w, bool local, const gdn_decay_desc* d) {
     const hipError_t e =
-        gdn::launch_decay_walk(w, kind, (int)d->key_dim, (int)d->value_dim, d->dtype == GDN_DTYPE_BF16);
+        gdn::launch_decay_walk(w, local, (int)d->key_dim, (int)d->value_dim, d->dtype == GDN_DTYPE_BF16);
     return e == hipSuccess ? GDN_OK : hip_fail(e, "decay attention launch");
 }
 
@@ -281,7 +281,7 @@ gdn_status gdn_decay_attn_fwd(const gdn_decay_desc* d, const void* q, const void
     float* state = reinterpret_cast<float*>(ws + L.state);
     if (L.tiles > 0) {
         const gdn::DecayWalk f = local_of(w, K, V, 1.f, state, reinterpret_cast<float*>(ws + L.dec));
-        if ((s = walk(f, gdn::DECAY_LOCAL, d)) != GDN_OK) return s;
+        if ((s = walk(f, true, d)) != GDN_OK) return s;
         const hipError_t e = gdn::launch_decay_join(join_of(d, f, h0, false, true));
         if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
     }
@@ -293,7 +293,7 @@ gdn_status gdn_decay_attn_fwd(const gdn_decay_desc* d, const void* q, const void
     w.seq_state = h0;
     w.seq_out = ht;
     w.out = o;
-    s = walk(w, gdn::DECAY_O, d);
+    s = walk(w, false, d);
     return s == GDN_OK ? api_ok() : s;
 }
 
@@ -330,45 +330,42 @@ gdn_status gdn_decay_attn_bwd(const gdn_decay_desc* d, const void* q, const void
     }
     const bool shared = v_heads(d) != d->num_heads;
 
-    gdn::DecayWalk w = w0;          // dq: forward over (do, v, k)
-    w.a = O;
-    w.b = V;
-    w.c = K;
-    w.x = Q;
-    w.in_scale = w.pair_scale = d->scale;
-    w.tile_state = at(L.state);
-    w.seq_state = h0;
-    w.tile_end = at(L.estate);
-    w.seq_end = dht;
-    w.ends = at(L.ends);
-    w.dots = at(L.dq);
-    w.out = dq;
-    w.out32 = shared ? at(L.dq32) : nullptr;
-    if ((s = walk(w, gdn::DECAY_DQ, d)) != GDN_OK) return s;
-
-    w = w0;                         // dk: backward over (v, do, q)
-    w.a = V;
-    w.b = O;
-    w.c = Q;
-    w.x = K;
-    w.pair_scale = w.up_scale = d->scale;
-    w.tile_state = at(L.estate);
-    w.seq_state = dht;
-    w.dots = at(L.dk);
-    w.out = dk;
-    w.out32 = shared ? at(L.dk32) : nullptr;
-    if ((s = walk(w, gdn::DECAY_DK, d)) != GDN_OK) return s;
-
-    w = w0;                         // dv: backward over (k, q, do)
-    w.a = K;
-    w.b = Q;
-    w.c = O;
-    w.pair_scale = w.up_scale = d->scale;
-    w.tile_state = at(L.estate);
-    w.seq_state = dht;
-    w.seq_out = dh0;
-    w.out = dv;
-    if ((s = walk(w, gdn::DECAY_DV, d)) != GDN_OK) return s;
+    gdn::DecayWalk wq = w0;         // dq: forward over (do, v, k)
+    wq.a = O;
+    wq.b = V;
+    wq.c = K;
+    wq.x = Q;
+    wq.in_scale = wq.pair_scale = d->scale;
+    wq.tile_state = at(L.state);
+    wq.seq_state = h0;
+    wq.tile_end = at(L.estate);
+    wq.seq_end = dht;
+    wq.ends = at(L.ends);
+    wq.dots = at(L.dq);
+    wq.out = dq;
+    wq.out32 = shared ? at(L.dq32) : nullptr;
+    gdn::DecayWalk wk = w0;         // dk: from the end over (v, do, q)
+    wk.a = V;
+    wk.b = O;
+    wk.c = Q;
+    wk.x = K;
+    wk.pair_scale = wk.up_scale = d->scale;
+    wk.tile_state = at(L.estate);
+    wk.seq_state = dht;
+    wk.dots = at(L.dk);
+    wk.out = dk;
+    wk.out32 = shared ? at(L.dk32) : nullptr;
+    gdn::DecayWalk wv = w0;         // dv: from the end over (k, q, do)
+    wv.a = K;
+    wv.b = Q;
+    wv.c = O;
+    wv.pair_scale = wv.up_scale = d->scale;
+    wv.tile_state = at(L.estate);
+    wv.seq_state = dht;
+    wv.seq_out = dh0;
+    wv.out = dv;
+    hipError_t e = gdn::launch_decay_grad(wq, wk, wv, (int)d->key_dim, (int)d->value_dim, d->dtype == GDN_DTYPE_BF16);
+    if (e != hipSuccess) return hip_fail(e, "decay attention gradient launch");
 
     gdn::DecayGate a;
     a.map = m;
@@ -383,7 +380,7 @@ gdn_status gdn_decay_attn_bwd(const gdn_decay_desc* d, const void* q, const void
     a.H = w0.H;
     a.tokens = L.tokens;
     a.stream = w0.stream;
-    hipError_t e = gdn::launch_decay_gate(a);
+    e = gdn::launch_decay_gate(a);
     if (e == hipSuccess && head) {
         gdn::RowSumLaunch r{at(L.dg), L.tokens, w0.H, 1, 1, dg, nullptr, reinterpret_cast<double*>(ws + L.sums),
                             w0.stream};

@@ -1,6 +1,7 @@
-// Linear attention with a decay for each head: the walks of segments alone, the
-// chaining of their states, the gates' gradient and the single-token step.  The
-// chunk walk itself, its mathematics and its figures are in k_decay.hpp.
+// Linear attention with a decay for each head: the gradients' walks of segments
+// alone, the chaining of the segments' states, the gates' gradient and the
+// single-token step.  The chunk walk itself, its mathematics and its figures are in
+// k_decay.hpp.
 #include "k_decay.hpp"
 
 namespace gdn {
@@ -29,17 +30,6 @@ hipError_t launch_decay_local2(const DecayWalk& f, const DecayWalk& r, int K, in
     if (K == 64 && V == 128) return bf ? local2<bf16, 64, 128>(f, r) : local2<float, 64, 128>(f, r);
     if (K == 128 && V == 64) return bf ? local2<bf16, 128, 64>(f, r) : local2<float, 128, 64>(f, r);
     if (K == 128 && V == 128) return bf ? local2<bf16, 128, 128>(f, r) : local2<float, 128, 128>(f, r);
-    return hipErrorInvalidValue;
-}
-
-hipError_t launch_decay_walk(const DecayWalk& p, DecayKind kind, int K, int V, bool bf) {
-    switch (kind) {
-        case DECAY_O: return launch_walk_o(p, K, V, bf);
-        case DECAY_DQ: return launch_walk_dq(p, K, V, bf);
-        case DECAY_DK: return launch_walk_dk(p, K, V, bf);
-        case DECAY_DV: return launch_walk_dv(p, K, V, bf);
-        case DECAY_LOCAL: return launch_walk_of<false, false, 0, true>(p, K, V, bf);
-    }
     return hipErrorInvalidValue;
 }
 
@@ -94,10 +84,11 @@ hipError_t launch_decay_join(const DecayJoin& a, const DecayJoin* b) {
 }
 
 // dg_t = <S, E> at the segment's end + the sum of the dots from t on, carried in 64
-// bits from 64 tokens to the next; 0 where the gate lets nothing through.  A wave takes
-// a segment of a head from its end.
-__global__ __launch_bounds__(64) void decay_gate_kernel(DecayGate a) {
-    const int lane = threadIdx.x;
+// bits from 256 tokens to the next; 0 where the gate lets nothing through.  A workgroup
+// takes a segment of a head from its end.
+__global__ __launch_bounds__(256) void decay_gate_kernel(DecayGate a) {
+    __shared__ float s_sum[2][4];
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
     const int64_t blk = blockIdx.x / a.H, h = blockIdx.x - blk * a.H;
     int64_t row0;
     int n;
@@ -113,27 +104,35 @@ __global__ __launch_bounds__(64) void decay_gate_kernel(DecayGate a) {
         row0 = (blk - a.tiles) * a.map.T;
         n = (int)a.map.T;
     }
-    if (n == 0) return;
-    double carry = a.ends[blk * a.H + h];
+    double carry = n > 0 ? (double)a.ends[blk * a.H + h] : 0.0;
     const float *dq = a.dq + h * a.tokens + row0, *dk = a.dk + h * a.tokens + row0;
     const float* g = a.g + row0 * a.gs + h;
-    int t = ((n - 1) & ~63) + 63 - lane;     // lane 0 takes the last token
-    float x = t < n ? dq[t] - dk[t] : 0.f, gt = t < n ? g[t * a.gs] : 0.f;
-    for (; t >= 0; t -= 64) {                // (alike in all lanes)
+    int first = (n + 255) / 256 * 256 - 256, turn = 0;     // thread 0 takes the last token
+    int t = first + 255 - tid;
+    float x = 0.f, gt = 0.f;
+    if (n > 0 && t < n) {
+        x = dq[t] - dk[t];
+        gt = g[t * a.gs];
+    }
+    for (; first >= 0; first -= 256, t -= 256, turn ^= 1) {
         const float now = scan64(x), gn = gt;
-        if (t >= 64) {                       // the next ones are on their way
-            x = dq[t - 64] - dk[t - 64];
-            gt = g[(t - 64) * a.gs];
+        if (first > 0) {                                   // the next ones are on their way
+            x = dq[t - 256] - dk[t - 256];
+            gt = g[(t - 256) * a.gs];
         }
-        if (t < n) a.dg[(row0 + t) * a.H + h] = gate_parts(gn).hi == -8192.f ? 0.f : (float)(carry + now);
-        carry += (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(now), 63));
+        if (lane == 63) s_sum[turn][w] = now;
+        __syncthreads();
+        const float s0 = s_sum[turn][0], s1 = s_sum[turn][1], s2 = s_sum[turn][2], s3 = s_sum[turn][3];
+        const double before = carry + (w > 0 ? (double)s0 : 0.0) + (w > 1 ? (double)s1 : 0.0) + (w > 2 ? (double)s2 : 0.0);
+        if (t < n) a.dg[(row0 + t) * a.H + h] = gate_parts(gn).hi == -8192.f ? 0.f : (float)(before + now);
+        carry += ((double)s0 + s1) + ((double)s2 + s3);
     }
 }
 
 hipError_t launch_decay_gate(const DecayGate& a) {
     const int64_t blocks = (a.tiles + a.singles) * a.H;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(decay_gate_kernel, dim3((unsigned)blocks), dim3(64), 0, a.stream, a);
+    hipLaunchKernelGGL(decay_gate_kernel, dim3((unsigned)blocks), dim3(256), 0, a.stream, a);
     return hipGetLastError();
 }
 

@@ -533,45 +533,10 @@ struct DecayBody {
     }
 };
 
-template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? (LOCAL ? 3 : 2) : 1) void decay_walk_kernel(DecayWalk p) {
-    typedef DecayBody<T, DA, DC, REV, TR, DOT, LOCAL> B;
-    __shared__ typename B::Shared s;
-    B::run(p, blockIdx.x, s);
-}
-
 // workgroups of a walk, a multiple of 8 heads' (see run)
 inline unsigned walk_blocks(const DecayWalk& p, bool local) {
     const int64_t units = (p.tiles + (local ? 0 : p.singles)) * (p.H / p.share);
     return (unsigned)((units + 7) / 8 * 8 * p.share);
 }
-
-template <typename T, int DA, int DC, bool REV, bool TR, int DOT, bool LOCAL>
-hipError_t launch_walk(const DecayWalk& p) {
-    const unsigned blocks = walk_blocks(p, LOCAL);
-    if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((decay_walk_kernel<T, DA, DC, REV, TR, DOT, LOCAL>), dim3(blocks), dim3(256), 0,
-                       p.stream, p);
-    return hipGetLastError();
-}
-
-// One walk for every type and head size: the launcher of a translation unit.
-template <bool REV, bool TR, int DOT, bool LOCAL>
-hipError_t launch_walk_of(const DecayWalk& p, int K, int V, bool bf) {
-#define GDN_DECAY_CASE(KK, VV)                                                                      \
-    if (K == KK && V == VV)                                                                         \
-        return bf ? launch_walk<bf16, TR ? VV : KK, TR ? KK : VV, REV, TR, DOT, LOCAL>(p)           \
-                  : launch_walk<float, TR ? VV : KK, TR ? KK : VV, REV, TR, DOT, LOCAL>(p);
-    GDN_DECAY_CASE(64, 64)
-    GDN_DECAY_CASE(64, 128)
-    GDN_DECAY_CASE(128, 64)
-    GDN_DECAY_CASE(128, 128)
-#undef GDN_DECAY_CASE
-    return hipErrorInvalidValue;
-}
-hipError_t launch_walk_o(const DecayWalk& p, int K, int V, bool bf);
-hipError_t launch_walk_dq(const DecayWalk& p, int K, int V, bool bf);
-hipError_t launch_walk_dk(const DecayWalk& p, int K, int V, bool bf);
-hipError_t launch_walk_dv(const DecayWalk& p, int K, int V, bool bf);
 
 }  // namespace gdn

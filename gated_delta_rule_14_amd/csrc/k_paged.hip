@@ -290,6 +290,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(Paged
             const int q = lane + 64 * i;
             *reinterpret_cast<u32x4*>(vt.p + R::at(q / UR, q % UR * R::U)) = vf[i];
         }
+        __builtin_amdgcn_wave_barrier();   // (the wave's own rows: its LDS accesses stay in order)
         f32x4 S[TH];
 #pragma unroll
         for (int h = 0; h < TH; ++h) {
