@@ -34,11 +34,10 @@ hipError_t launch_decay_local2(const DecayWalk& f, const DecayWalk& r, int K, in
 }
 
 // S_0 = first, S_{j+1} = dec_j S_j + local_j over a sequence's segments; S_j takes
-// the place of local_j.  A workgroup takes 1024 elements of a sequence's state, by
-// the block of its first segment; the next segment's are on their way meanwhile.
+// the place of local_j.  A workgroup takes 1024 elements of a sequence's state.
 __device__ __forceinline__ void join(const DecayJoin& a, unsigned block) {
     const int64_t per = (a.KV + 1023) / 1024, hb = a.H * per;
-    const int64_t c = block / hb, rest = block - c * hb, h = rest / per;
+    const int64_t i = block / hb, c = a.map.table ? i : i * a.map.nt, rest = block - i * hb, h = rest / per;
     const int64_t e = (rest - h * per) * 1024 + threadIdx.x * 4;
     const Tile t = tile_of(a.map, c);
     if (t.n == 0 || t.j != 0 || e >= a.KV) return;
@@ -55,18 +54,29 @@ __device__ __forceinline__ void join(const DecayJoin& a, unsigned block) {
             s = *reinterpret_cast<const f32x4*>(first + e);
         }
     }
-    const int64_t step = a.rev ? -1 : 1;
-    int64_t at = c + (a.rev ? t.nt - 1 : 0);
-    f32x4 next = *reinterpret_cast<const f32x4*>(a.state + (at * a.H + h) * a.KV + e);
-    for (int j = 0; j < t.nt; ++j, at += step) {
-        f32x4* p = reinterpret_cast<f32x4*>(a.state + (at * a.H + h) * a.KV + e);
-        const f32x4 own = next;
-        if (j + 1 < t.nt) next = *reinterpret_cast<const f32x4*>(a.state + ((at + step) * a.H + h) * a.KV + e);
-        *p = s;
-        if (j + 1 < t.nt) {            // (the last one walked has no local state)
-            const float d = a.dec[at * a.H + h];
+    // eight segments' states on their way at a time: one after the other they would each
+    // be waited for
+    constexpr int U = 8;
+    const int64_t step = a.rev ? -1 : 1, at = c + (a.rev ? t.nt - 1 : 0);
+    for (int j0 = 0; j0 < t.nt; j0 += U) {
+        f32x4 own[U];
+        float d[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] = fmaf(d, s[i], own[i]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = (at + (j0 + u) * step) * a.H + h;
+            if (j0 + u + 1 < t.nt) {       // (the last one walked has no local state)
+                own[u] = *reinterpret_cast<const f32x4*>(a.state + row * a.KV + e);
+                d[u] = a.dec[row];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u >= t.nt) break;
+            *reinterpret_cast<f32x4*>(a.state + ((at + (j0 + u) * step) * a.H + h) * a.KV + e) = s;
+            if (j0 + u + 1 < t.nt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = fmaf(d[u], s[i], own[u][i]);
+            }
         }
     }
 }
@@ -76,8 +86,9 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecayJoin a, DecayJoin 
 }
 
 hipError_t launch_decay_join(const DecayJoin& a, const DecayJoin* b) {
-    const int64_t half = a.tiles * a.H * ((a.KV + 1023) / 1024);
-    if (half == 0) return hipSuccess;
+    if (a.tiles == 0) return hipSuccess;
+    // a sequence's first segment: every table row might be one
+    const int64_t half = (a.map.table ? a.tiles : a.map.N) * a.H * ((a.KV + 1023) / 1024);
     hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)(b ? 2 * half : half)), dim3(256), 0, a.stream, a, b ? *b : a,
                        (unsigned)half);
     return hipGetLastError();
