@@ -39,12 +39,14 @@ gdn_status check_decay(const gdn_decay_desc* d, bool packed) {
 }
 
 // Segments that long sequences are cut into, each walked by a workgroup per state
-// head: as long as leaves the chip two workgroups to a compute unit, at most 4096
-// tokens (a longer walk would end alone; 64 sequences of 100 to 4000 tokens, 16 heads of
-// 128: 642 us, with 2048 894, with 8192 637; 65536 and 6 x 10000: 851, 772, 852), and at
-// least as many as make a walk worth the two more launches: 128, or 64 in fp32, whose chunk takes three times as long (3 x 1001
-// tokens of 6 heads in fp32, training step: 186 us with 64, 236 with 256; 300 tokens
-// of 4 heads in bf16, forward: 22 us with 128, 32 with 256).
+// head: as long as leaves the chip two workgroups to a compute unit (4 x 4096 tokens of
+// 16 heads, forward: 118 us, with half as many 120, with 768 143, with 1024 145), at
+// most 4096 tokens (a longer walk would end alone; 64 sequences of 100 to 4000 tokens,
+// 16 heads of 128: 642 us, with 2048 894, with 8192 637; 65536 and 6 x 10000: 851, 772,
+// 852; 65536 and 15 of up to 8192, 32 heads: 1153, 1223, 1218), and at least as many as
+// make a walk worth the two more launches: 128, or 64 in fp32, whose chunk takes three
+// times as long (3 x 1001 tokens of 6 heads in fp32, training step: 186 us with 64, 236
+// with 256; 300 tokens of 4 heads in bf16, forward: 22 us with 128, 32 with 256).
 int decay_tile(const gdn_decay_desc* d) {
     const double tokens = (double)d->batch * (double)d->seq_len;
     const int64_t want = (int64_t)(tokens * (double)v_heads(d) / 512.0);
