@@ -439,7 +439,29 @@ struct DecayBody {
             }
 
             if constexpr (!LOCAL) {
+                // A value of c that is not finite has made its column of S so.  It may not reach, as 0
+                // times itself, the outputs that do not see it: such a chunk goes token by token.
+                bool odd = false;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) odd |= !(__builtin_fabsf(S[0][ct][0]) < INFINITY);
                 lds_barrier();   // the pairs of all tile rows are there
+                if (__builtin_expect(__any(odd), 0)) {
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const int i = 16 * it + rr;
+#pragma unroll 1
+                        for (int m = REV ? i : 0; m <= (REV ? min(63, t.n - first_of(j) - 1) : i); ++m) {
+                            const int at = (m & 32) + 8 * (m >> 2 & 3) + 4 * (m >> 4 & 1) + (m & 3);   // as put
+                            const float y = Elem<T>::load(s.pairs + i * PW + at);
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) {
+                                const f32x4 v = rc.row4(m, 16 * CT * w + 4 * CT * gg + 4 * ct);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) O[it][ct][e] = fmaf(y, v[e], O[it][ct][e]);
+                            }
+                        }
+                    }
+                } else {
 #pragma unroll
                 for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -456,6 +478,7 @@ struct DecayBody {
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) O[it][ct] = E8::mma(cf[js][ct], b, O[it][ct]);
                     }
+                }
                 const int64_t t0 = first_of(j);
                 const int n = min(64, t.n - (int)t0);
                 const int64_t first = ((t.row0 + t0) * p.H + h) * DC;

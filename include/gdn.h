@@ -688,7 +688,10 @@ gdn_status gdn_short_conv_step(const gdn_conv_desc *d, const void *x, const floa
  * tokens (GDN_DECAY_PER_HEAD).  With num_v_heads = H_V, a multiple of H, state
  * head h uses head h / (H_V / H) of q and k.  Any g is taken: a gate of
  * -infinity (or below -104, where exp gives 0 in fp32) cuts the sequence, and
- * growing gates are followed as far as their products stay finite.
+ * growing gates are followed as far as their products stay finite.  A value that
+ * is not finite (as behind the end of a padded sequence) does not reach the
+ * outputs of tokens before it; of the gradients, dg alone takes it anywhere in its
+ * sequence's head.
  *
  * Rows of q, k and v may lie in wider tensors: a token stride and a head stride
  * each (elements, multiples of 8; 0: dense), a token's rows below 2^24 elements

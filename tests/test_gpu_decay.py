@@ -269,3 +269,36 @@ def test_refusals(gpu_lib):
 def test_no_sequences_step(gpu_lib):
     z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
     assert gpu_lib.decay_attn_step(z(0, 1, 64), z(0, 1, 64), z(0, 2, 64), z(0, 2), z(0, 2, 64, 64)).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,at", [(50, 30), (300, 290), (700, 200)])
+def test_values_that_are_not_finite(gpu_lib, dt, bad, T, at):
+    """A value that is not finite, in one head of one sequence, reaches what sees it and nothing else."""
+    gdn = gpu_lib
+    d = inputs(11, 2, T, 2, 2, 64, 128, dt)
+    want, err = ref.decay(d["q"], d["k"], d["v"], d["g"], None, d["h0"], None, d["do"], d["dht"])
+    for name in ("q", "k", "v", "do"):
+        x = dict(d, **{name: d[name].clone()})
+        x[name][1, at, 1, 7] = bad
+        c = {n: t.cuda() if torch.is_tensor(t) else t for n, t in x.items()}
+        o, ht = gdn.decay_attn_fwd(c["q"], c["k"], c["v"], c["g"], h0=c["h0"])
+        b = gdn.decay_attn_bwd(c["q"], c["k"], c["v"], c["g"], c["do"], h0=c["h0"], dht=c["dht"])
+        torch.cuda.synchronize()
+        got = dict(b, o=o, ht=ht)
+        for n in want:                     # the other sequence and the other head
+            for part in ((0, slice(None)), (1, slice(None), 0) if n[0] in "od" and n != "dh0" else (1, 0)):
+                layer_ref.check(got[n][part], want[n][part], err[n][part], "%s of bad %s" % (n, name))
+        before, after = (1, slice(0, at), 1), (1, slice(at + 1, T), 1)
+        clean = dict(q=[("o", before), ("o", after), ("dq", before), ("dq", after), ("dk", after), ("dv", after)],
+                     k=[("o", before), ("dq", before), ("dk", before), ("dk", after), ("dv", before), ("dv", after)],
+                     v=[("o", before), ("dq", before), ("dk", before), ("dk", after), ("dv", before), ("dv", after)],
+                     do=[("o", (1, slice(None), 1)), ("dq", before), ("dq", after), ("dk", after), ("dv", after)])[name]
+        for n, part in clean:
+            layer_ref.check(got[n][part], want[n][part], err[n][part], "%s of bad %s" % (n, name))
+        seen = dict(q=[("o", (1, at, 1)), ("dv", (1, slice(0, at + 1), 1))], k=[("o", (1, at, 1)), ("ht", (1, 1, 7))],
+                    v=[("o", (1, slice(at, T), 1, 7)), ("ht", (1, 1, slice(None), 7))],
+                    do=[("dq", (1, at, 1)), ("dv", (1, slice(0, at + 1), 1, 7))])[name]
+        for n, part in seen:
+            assert not bool(torch.isfinite(got[n][part]).any()), (n, name)
