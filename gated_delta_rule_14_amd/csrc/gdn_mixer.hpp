@@ -27,6 +27,7 @@ struct DecayWalk {
     int64_t gs = 0;
     float in_scale = 1.f, pair_scale = 1.f, up_scale = 1.f;
     const float* tile_state = nullptr;   // [tiles][H][K][V] states entering the segments
+    int chain = 0;                       //   or, of sequences of up to `chain` segments, these alone
     const float* seq_state = nullptr;    // [N][H][K][V] entering whole sequences, or nullptr
     float* seq_out = nullptr;     // [N][H][K][V] states leaving the sequences, or nullptr
     const float *tile_end = nullptr, *seq_end = nullptr;   // what the leaving states are multiplied
@@ -57,6 +58,7 @@ struct DecayJoin {
     int V;                        // with own_order the states' elements are in the forward walk's
     bool own_order;               //   order, but those of `first`, which are [K][V]
     bool rev;                     // from the last segment to the first
+    int chain;                    // sequences of up to so many segments are left to the walk
     hipStream_t stream;
 };
 hipError_t launch_decay_join(const DecayJoin& a, const DecayJoin* b = nullptr);   // b: another one of its sizes

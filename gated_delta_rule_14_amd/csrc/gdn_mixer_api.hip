@@ -164,6 +164,7 @@ gdn::DecayJoin join_of(const gdn_decay_desc* d, const gdn::DecayWalk& w, const f
     j.H = w.H;
     j.KV = d->key_dim * d->value_dim;
     j.rev = rev;
+    j.chain = w.chain;
     j.stream = w.stream;
     return j;
 }
@@ -282,10 +283,14 @@ gdn_status gdn_decay_attn_fwd(const gdn_decay_desc* d, const void* q, const void
     const gdn::HeadRows V = rows_of(d, v, true, d->v_stride, d->v_head_stride);
     float* state = reinterpret_cast<float*>(ws + L.state);
     if (L.tiles > 0) {
-        const gdn::DecayWalk f = local_of(w, K, V, 1.f, state, reinterpret_cast<float*>(ws + L.dec));
+        w.chain = 8;
+        w.dec = reinterpret_cast<float*>(ws + L.dec);
+        const gdn::DecayWalk f = local_of(w, K, V, 1.f, state, w.dec);
         if ((s = walk(f, true, d)) != GDN_OK) return s;
-        const hipError_t e = gdn::launch_decay_join(join_of(d, f, h0, false, true));
-        if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
+        if (d->seq_len > (int64_t)w.chain * L.tile) {
+            const hipError_t e = gdn::launch_decay_join(join_of(d, f, h0, false, true));
+            if (e != hipSuccess) return hip_fail(e, "decay attention state launch");
+        }
     }
     w.a = Q;
     w.b = K;

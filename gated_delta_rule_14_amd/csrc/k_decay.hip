@@ -40,7 +40,7 @@ __device__ __forceinline__ void join(const DecayJoin& a, unsigned block) {
     const int64_t i = block / hb, c = a.map.table ? i : i * a.map.nt, rest = block - i * hb, h = rest / per;
     const int64_t e = (rest - h * per) * 1024 + threadIdx.x * 4;
     const Tile t = tile_of(a.map, c);
-    if (t.n == 0 || t.j != 0 || e >= a.KV) return;
+    if (t.n == 0 || t.j != 0 || t.nt <= a.chain || e >= a.KV) return;
     f32x4 s = zero4();
     if (a.first) {
         const float* first = a.first + (t.seq * a.H + h) * a.KV;

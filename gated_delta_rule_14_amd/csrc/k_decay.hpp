@@ -228,15 +228,16 @@ struct DecayBody {
             }
         }
         f32x4 S[KT][CT];
+        const bool chained = OWN && !LOCAL && !single && t.nt <= p.chain;
         const float* sin = LOCAL ? nullptr
-                           : single ? (p.seq_state ? p.seq_state + (t.seq * p.H + h) * KV : nullptr)
+                           : single || chained ? (p.seq_state ? p.seq_state + (t.seq * p.H + h) * KV : nullptr)
                                     : p.tile_state + (blk * p.H + h) * KV;
         if (!sin) {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) S[kt][ct] = zero4();
-        } else if (OWN && !single) {
+        } else if (OWN && !single && !chained) {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -254,6 +255,21 @@ struct DecayBody {
                         for (int e = 0; e < 4; ++e) S[kt][ct][e] = sin[state_at(w, lane, kt, ct, e)];
                     }
                 }
+        }
+        if (chained) {       // as launch_decay_join would
+            const int64_t step = p.H * KV;
+            const float *own = p.tile_state + ((blk - t.j) * p.H + h) * KV, *d = p.dec + (blk - t.j) * p.H + h;
+            for (int j = 0; j < t.j; ++j, own += step, d += p.H) {
+                const float dj = *d;
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const f32x4 x = *reinterpret_cast<const f32x4*>(own + own_at(w, lane, kt, ct));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) S[kt][ct][e] = fmaf(dj, S[kt][ct][e], x[e]);
+                    }
+            }
         }
         float total = 1.f;   // LOCAL: decay of the segment
 
