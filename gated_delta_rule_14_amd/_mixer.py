@@ -207,21 +207,20 @@ def _attn_plan(*fields):
 
 def _pages(k_cache, v_cache, page_table, lens, like, heads, D, dev):
     """Checks of a cache [pages, page_size, heads, D] and its table: the plan of gdn_pages."""
-    sh = k_cache.shape
+    sh, ks, vs, ts, dt = k_cache.shape, k_cache.stride(), v_cache.stride(), page_table.shape, like.dtype
     if len(sh) != 4 or v_cache.shape != sh or sh[2] != heads or sh[3] != D:
         raise ValueError("k_cache and v_cache must be [pages, page_size, %d, %d], got %s, %s"
                          % (heads, D, tuple(sh), tuple(v_cache.shape)))
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != like.dtype or t.device != dev:
-            raise ValueError("%s must have the type and device of the activations" % name)
-        if t.stride(3) != 1:
-            raise ValueError("%s must be dense in its last dimension" % name)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [N, max_pages], got %s" % (tuple(page_table.shape),))
-    N, M = page_table.shape
-    _dense(page_table, "page_table", (N, M), dev, torch.int32)
+    if k_cache.dtype is not dt or v_cache.dtype is not dt or k_cache.device != dev or v_cache.device != dev:
+        raise ValueError("k_cache and v_cache must have the type and device of the activations")
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("k_cache and v_cache must be dense in their last dimension")
+    if len(ts) != 2:
+        raise ValueError("page_table must be [N, max_pages], got %s" % (tuple(ts),))
+    N, M = ts
+    _dense(page_table, "page_table", ts, dev, torch.int32)
     _dense(lens, "lens", (N,), dev, torch.int64)
-    return _pages_plan(N, M, sh[0], sh[1], *k_cache.stride()[:3], *v_cache.stride()[:3]), N
+    return _pages_plan(N, M, sh[0], sh[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), N
 
 
 def _look(k_cache, page_table, lens, T, cu_seqlens, stream, dev):
@@ -306,7 +305,7 @@ def _attn(q, k_cache, v_cache, page_table, lens, scale, window):
     c, N = _pages(k_cache, v_cache, page_table, lens, q, Hk, D, dev)
     if n != N:
         raise ValueError("page_table has %d rows for %d sequences" % (N, n))
-    qt, qh = _heads(q[:, None], "q") if n else (0, 0)
+    qt, qh = _rows(q, "q") if n else (0, 0)
     return _attn_plan(N, Hq, Hk, D, qt, qh, int(window), _code(q, "q"),
                       float(D ** -0.5 if scale is None else scale)), c, dev
 
