@@ -302,3 +302,15 @@ def test_values_that_are_not_finite(gpu_lib, dt, bad, T, at):
                     do=[("dq", (1, at, 1)), ("dv", (1, slice(0, at + 1), 1, 7))])[name]
         for n, part in seen:
             assert not bool(torch.isfinite(got[n][part]).any()), (n, name)
+
+
+@pytest.mark.parametrize("T", [500, 1000, 2500])
+def test_state_carried_in_place(gpu_lib, T):
+    """ht in h0's place: the bits of a call with its own, of sequences of a few segments and of many."""
+    gdn = gpu_lib
+    c = cuda(inputs(12, 2, T, 2, 2, 64, 128))
+    o, ht = gdn.decay_attn_fwd(c["q"], c["k"], c["v"], c["g"], h0=c["h0"])
+    h = c["h0"].clone()
+    o2, _ = gdn.decay_attn_fwd(c["q"], c["k"], c["v"], c["g"], h0=h, ht=h)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(ht, h)
