@@ -158,6 +158,8 @@ struct GvaSumLaunch {
     int K;
     bool bf16;
     hipStream_t stream;
+    const float* part2 = nullptr;   // another sum of the same sizes
+    void* out2 = nullptr;
 };
 
 // The fused forward (bf16 q/k/v, scalar gate, K and V each 64 or 128, C = 64):

@@ -72,6 +72,7 @@ struct DecayGate {
     const float* g;
     int64_t gs;
     float* dg;                    // [tokens][H]
+    float* part;                  // or the segments' sums of it [tiles + singles][H]
     int64_t H, tokens;
     hipStream_t stream;
 };

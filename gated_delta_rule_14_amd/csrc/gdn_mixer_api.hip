@@ -87,8 +87,8 @@ DecayLayout decay_layout(const gdn_decay_desc* d, bool backward) {
         L.dq = take((size_t)L.tokens * H * 4);
         L.dk = take((size_t)L.tokens * H * 4);
         L.ends = take((size_t)(L.tiles + L.singles) * H * 4);
-        L.dg = take(head ? (size_t)L.tokens * H * 4 : 0);
-        L.sums = take(head ? sums_bytes(L.tokens, H) : 0);
+        L.dg = take(head ? (size_t)(L.tiles + L.singles) * H * 4 : 0);
+        L.sums = take(head ? sums_bytes(L.tiles + L.singles, H) : 0);
         L.dq32 = take(shared ? (size_t)L.tokens * H * d->key_dim * 4 : 0);
         L.dk32 = take(shared ? (size_t)L.tokens * H * d->key_dim * 4 : 0);
     }
@@ -100,8 +100,8 @@ gdn_status check_decay_grid(const gdn_decay_desc* d, const DecayLayout& L) {
     const double H = (double)v_heads(d), per = (double)(d->key_dim * d->value_dim / 1024);
     gdn_status s = check_grid(3 * ((double)L.tiles + (double)L.singles + 8) * H, 256);
     if (s == GDN_OK) s = check_grid(2 * ((double)L.tiles + 8) * H * per, 256);
-    // (the sums of dq and dk over shared heads: four elements to a thread)
-    return s != GDN_OK ? s : check_grid((double)L.tokens * (double)(d->num_heads * d->key_dim / 4) / 256, 256);
+    // (the sums of dq and dk over shared heads: four elements to a thread, both in one launch)
+    return s != GDN_OK ? s : check_grid((double)L.tokens * (double)(d->num_heads * d->key_dim / 2) / 256, 256);
 }
 
 // rows of q, k (H heads) or v, o (H_V heads), as wide as `w`
@@ -386,13 +386,14 @@ gdn_status gdn_decay_attn_bwd(const gdn_decay_desc* d, const void* q, const void
     a.ends = at(L.ends);
     a.g = g;
     a.gs = w0.gs;
-    a.dg = head ? at(L.dg) : dg;
+    a.dg = dg;
+    a.part = head ? at(L.dg) : nullptr;
     a.H = w0.H;
     a.tokens = L.tokens;
     a.stream = w0.stream;
     e = gdn::launch_decay_gate(a);
     if (e == hipSuccess && head) {
-        gdn::RowSumLaunch r{at(L.dg), L.tokens, w0.H, 1, 1, dg, nullptr, reinterpret_cast<double*>(ws + L.sums),
+        gdn::RowSumLaunch r{at(L.dg), L.tiles + L.singles, w0.H, 1, 1, dg, nullptr, reinterpret_cast<double*>(ws + L.sums),
                             w0.stream};
         e = gdn::launch_row_sum(r);
     }
@@ -406,10 +407,9 @@ gdn_status gdn_decay_attn_bwd(const gdn_decay_desc* d, const void* q, const void
         r.stream = w0.stream;
         r.part = at(L.dq32);
         r.out = dq;
+        r.part2 = at(L.dk32);
+        r.out2 = dk;
         e = gdn::launch_gva_sum(r);
-        r.part = at(L.dk32);
-        r.out = dk;
-        if (e == hipSuccess) e = gdn::launch_gva_sum(r);
     }
     return e == hipSuccess ? api_ok() : hip_fail(e, "decay attention gradient launch");
 }

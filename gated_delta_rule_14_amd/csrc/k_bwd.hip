@@ -1061,10 +1061,11 @@ __global__ __launch_bounds__(256) void gva_sum_kernel(GvaSumLaunch a) {
     if (i >= a.rows * per_row) return;
     const int64_t row = i / per_row, rest = i - row * per_row;
     const int64_t hq = rest / (a.K / 4), c = (rest - hq * (a.K / 4)) * 4;
+    const float* part = blockIdx.y ? a.part2 : a.part;
     f32x4 acc = zero4();
     for (int64_t u = 0; u < m; ++u)
-        acc += *reinterpret_cast<const f32x4*>(a.part + (row * a.H + hq * m + u) * a.K + c);
-    store4(static_cast<T*>(a.out) + (row * a.Hq + hq) * a.K + c, acc);
+        acc += *reinterpret_cast<const f32x4*>(part + (row * a.H + hq * m + u) * a.K + c);
+    store4(static_cast<T*>(blockIdx.y ? a.out2 : a.out) + (row * a.Hq + hq) * a.K + c, acc);
 }
 
 // dA_log[h] and ddt_bias[h]: one workgroup per head sums the per-chunk
@@ -1192,7 +1193,7 @@ hipError_t launch_l2norm_bwd(const L2BwdLaunch& a) {
 hipError_t launch_gva_sum(const GvaSumLaunch& a) {
     const int64_t n = a.rows * a.Hq * (a.K / 4);
     if (n <= 0) return hipSuccess;
-    const dim3 grid((unsigned)((n + 255) / 256));
+    const dim3 grid((unsigned)((n + 255) / 256), a.part2 ? 2 : 1);
     if (a.bf16)
         hipLaunchKernelGGL(gva_sum_kernel<bf16>, grid, dim3(256), 0, a.stream, a);
     else

@@ -314,3 +314,10 @@ def test_state_carried_in_place(gpu_lib, T):
     o2, _ = gdn.decay_attn_fwd(c["q"], c["k"], c["v"], c["g"], h0=h, ht=h)
     torch.cuda.synchronize()
     assert torch.equal(o, o2) and torch.equal(ht, h)
+
+
+@pytest.mark.parametrize("lengths", [(0,), (0, 5, 0), (3,) * 600, (700, 0, 40)])
+def test_gate_per_head_over_sequences(gpu_lib, lengths):
+    """dg of a gate for each head sums over all tokens: none, few, many sequences, segments."""
+    d = inputs(13, 1, sum(lengths), 1, 2, 64, 64, "f32", N=len(lengths), per_head=True)
+    both(gpu_lib, d, offsets(lengths))
