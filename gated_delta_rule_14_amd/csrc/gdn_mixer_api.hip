@@ -43,14 +43,14 @@ gdn_status check_decay(const gdn_decay_desc* d, bool packed) {
 // 16 heads, forward: 118 us, with half as many 120, with 768 143, with 1024 145), at
 // most 4096 tokens (a longer walk would end alone; 64 sequences of 100 to 4000 tokens,
 // 16 heads of 128: 642 us, with 2048 894, with 8192 637; 65536 and 6 x 10000: 851, 772,
-// 852; 65536 and 15 of up to 8192, 32 heads: 1153, 1223, 1218), and at least as many as
-// make a walk worth the two more launches: 128, or 64 in fp32, whose chunk takes three
-// times as long (3 x 1001 tokens of 6 heads in fp32, training step: 186 us with 64, 236
-// with 256; 300 tokens of 4 heads in bf16, forward: 22 us with 128, 32 with 256).
+// 852; 65536 and 15 of up to 8192, 32 heads: 1153, 1223, 1218), and at least 128 (3 x 1001
+// tokens of 6 heads in fp32, training step: 126 us, with 64 or 256 144), or 64 where the
+// gradients' three walks then have a compute unit for each workgroup (4 heads of 128,
+// forward and backward: 300 tokens in bf16 16 and 29 us, with 128 19 and 36; in fp32 33 and
+// 45, with 128 47 and 66; beyond, 2 x 2048 tokens in bf16 34 and 62, with 128 33 and 52).
 int decay_tile(const gdn_decay_desc* d) {
-    const double tokens = (double)d->batch * (double)d->seq_len;
-    const int64_t want = (int64_t)(tokens * (double)v_heads(d) / 512.0);
-    const int64_t least = d->dtype == GDN_DTYPE_BF16 ? 128 : 64;
+    const double work = (double)d->batch * (double)d->seq_len * (double)v_heads(d);
+    const int64_t want = (int64_t)(work / 512.0), least = 3 * work <= 256 * 64 ? 64 : 128;
     return (int)std::min((int64_t)4096, std::max(least, (want + 63) / 64 * 64));
 }
 
