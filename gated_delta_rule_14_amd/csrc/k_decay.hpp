@@ -24,16 +24,17 @@
 // whose layout is that of an operand over its own rows, so S never passes
 // through LDS.  The pairs' products of the chunk are made once, a tile row to a
 // wave, and handed round in LDS.  Long sequences are cut into segments: a first
-// walk makes each segment's own state, launch_decay_join chains them, and the
-// segments then run side by side.
+// walk makes each segment's own state, launch_decay_join chains them (of few
+// segments the walk itself), and the segments then run side by side.
 //
 // What bounds it: two workgroups fill a compute unit's registers and LDS, two
 // waves to a SIMD, which take turns at the matrix unit, the vector ALU and LDS
 // (of 64 tokens of a head the output walk has 150 matrix and 600 vector
 // instructions a wave).  16 heads of 128 x 128 in bf16, 16384 tokens: segments'
-// states 35 us (134 MB read, 3.8 TB/s), output 66 us (268 MB, 4.1 TB/s), the three
-// gradient walks together 250 us (40% of it matrix-unit and vector issue each, LDS
-// 45%).  Eight waves of 16 columns each: 76 us for the output instead of 68, each
+// states 35 us (134 MB read, 3.8 TB/s), output 66 us (268 MB, 4.1 TB/s; 70 where it
+// chains the states of eight segments as well), the three gradient walks together
+// 250 us, the matrix unit busy for a quarter of it, the vector ALU and LDS for about
+// two fifths each.  Eight waves of 16 columns each: 76 us for the output instead of 68, each
 // then reads all of a and b for half as many products.
 //
 // Roundings: products are of the inputs' type, sums in 32 bits.  With bf16 the
