@@ -102,6 +102,20 @@ __device__ __forceinline__ float scan64(float x) {
     x = dpp_from<0x143, 0xc>(x);   // row_bcast:31 into rows 2 and 3
     return x;
 }
+__device__ __forceinline__ float lane_of(float x, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+// Sum of the lanes behind each lane: of its row of 16 by DPP row shifts, then the rows behind.
+__device__ __forceinline__ float behind64(float x, int lane) {
+    x = dpp_from<0x101, 0xf>(x);   // row_shl:1, 2, 4, 8
+    x = dpp_from<0x102, 0xf>(x);
+    x = dpp_from<0x104, 0xf>(x);
+    x = dpp_from<0x108, 0xf>(x);
+    const float t1 = lane_of(x, 16), t2 = lane_of(x, 32), t3 = lane_of(x, 48);
+    x += lane < 16 ? t1 + (t2 + t3) : lane < 32 ? t2 + t3 : lane < 48 ? t3 : 0.f;
+    const float y = __shfl_down(x, 1, 64);
+    return lane < 63 ? y : 0.f;
+}
 
 // What the waves need of a chunk's gates: sums up to each token (reversed walks:
 // from behind it), the factors of the state in and out, and of the whole chunk.
@@ -115,17 +129,14 @@ template <bool REV>
 __device__ __forceinline__ void make_gates(ChunkGates& s, float g, int n, float in_scale, float up_scale, int lane) {
     const bool on = lane < n;
     const GateParts p = gate_parts(on ? g : 0.f);
-    float hi = scan64(p.hi), lo = scan64(p.lo);
-    const float th = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), 63));
-    const float tl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), 63));
-    if (REV) {
-        hi = th - hi;
-        lo = tl - lo;
-    }
+    const float ph = scan64(p.hi), pl = scan64(p.lo), th = lane_of(ph, 63), tl = lane_of(pl, 63);
+    // (from behind a sum of its own, not what is left of the whole: a gate that is not finite
+    // may not reach the tokens behind it)
+    const float hi = REV ? behind64(p.hi, lane) : ph, lo = REV ? behind64(p.lo, lane) : pl;
     s.hi[lane] = on ? hi : REV ? 8192.f * 64 : -8192.f * 64;
     s.lo[lane] = lo;
     s.in[lane] = on ? in_scale * exp2_hw(hi + lo) : 0.f;
-    s.out[lane] = on ? up_scale * exp2_hw((th - hi) + (tl - lo)) : 0.f;
+    s.out[lane] = on ? up_scale * (REV ? exp2_hw(ph + pl) : exp2_hw((th - hi) + (tl - lo))) : 0.f;
     if (lane == 0) s.dec = exp2_hw(th + tl);
 }
 

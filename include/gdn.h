@@ -691,7 +691,7 @@ gdn_status gdn_short_conv_step(const gdn_conv_desc *d, const void *x, const floa
  * growing gates are followed as far as their products stay finite.  A value that
  * is not finite (as behind the end of a padded sequence) does not reach the
  * outputs of tokens before it; of the gradients, dg alone takes it anywhere in its
- * sequence's head.
+ * sequence's head.  Nor does such a gate reach dk and dv from its own token on.
  *
  * Rows of q, k and v may lie in wider tensors: a token stride and a head stride
  * each (elements, multiples of 8; 0: dense), a token's rows below 2^24 elements
