@@ -30,8 +30,10 @@ struct DecayWalk {
     int chain = 0;                       //   or, of sequences of up to `chain` segments, these alone
     const float* seq_state = nullptr;    // [N][H][K][V] entering whole sequences, or nullptr
     float* seq_out = nullptr;     // [N][H][K][V] states leaving the sequences, or nullptr
-    const float *tile_end = nullptr, *seq_end = nullptr;   // what the leaving states are multiplied
-    float* ends = nullptr;        //   with, and the sums: [tiles + singles][H]
+    // the gradients behind segments and whole sequences, and their products with the state that
+    // leaves the chunk before the last one, decayed to the end: [tiles + singles][H]
+    const float *tile_end = nullptr, *seq_end = nullptr;
+    float* ends = nullptr;
     void* out = nullptr;          // [tokens][H][DC], element type
     float* out32 = nullptr;       // or in 32 bits
     float* dots = nullptr;        // [H][tokens]

@@ -95,8 +95,10 @@ hipError_t launch_decay_join(const DecayJoin& a, const DecayJoin* b) {
     return hipGetLastError();
 }
 
-// dg_t = <S, E> at the segment's end + the sum of the dots from t on, carried in 64
-// bits from 256 tokens to the next; 0 where the gate lets nothing through.  A workgroup
+// dg_t = the product of the state before the segment's last chunk and the gradient behind
+// it, plus the dots of dq and dk that the walks left (k_decay.hpp): from t on those of dq,
+// less those of dk, of the last chunk those of dk before t instead.  Carried in 64 bits from 256
+// tokens to the next; 0 where the gate lets nothing through.  A workgroup
 // takes a segment of a head from its end.  With one gate for each head only the
 // segment's sum goes out (3 x 1001 tokens of 6 heads, with the sum over the segments:
 // 16 -> 9 us).
@@ -124,13 +126,15 @@ __global__ __launch_bounds__(256) void decay_gate_kernel(DecayGate a) {
     const float* g = a.g + row0 * a.gs + h;
     int first = (n + 255) / 256 * 256 - 256, turn = 0;     // thread 0 takes the last token
     int t = first + 255 - tid;
-    float x = 0.f, gt = 0.f;
+    float x = 0.f, gt = 0.f, before_t = 0.f;
     double all = 0.0;
+    const bool end = t >> 6 == (n - 1) >> 6;               // (a wave's 64 tokens are a chunk)
     if (n > 0 && t < n) {
-        x = dq[t] - dk[t];
+        x = end ? dq[t] : dq[t] - dk[t];
         gt = g[t * a.gs];
     }
-    for (; first >= 0; first -= 256, t -= 256, turn ^= 1) {
+    if (n > 0 && end) before_t = behind64(t < n ? dk[t] : 0.f, lane);   // lanes behind: tokens before
+    for (; first >= 0; first -= 256, t -= 256, turn ^= 1, before_t = 0.f) {
         const float now = scan64(x), gn = gt;
         if (first > 0) {                                   // the next ones are on their way
             x = dq[t - 256] - dk[t - 256];
@@ -140,7 +144,7 @@ __global__ __launch_bounds__(256) void decay_gate_kernel(DecayGate a) {
         __syncthreads();
         const float s0 = s_sum[turn][0], s1 = s_sum[turn][1], s2 = s_sum[turn][2], s3 = s_sum[turn][3];
         const double before = carry + (w > 0 ? (double)s0 : 0.0) + (w > 1 ? (double)s1 : 0.0) + (w > 2 ? (double)s2 : 0.0);
-        const double y = gate_parts(gn).hi == -8192.f ? 0.0 : before + now;
+        const double y = gate_parts(gn).hi == -8192.f ? 0.0 : before + now + before_t;
         if (t < n) {
             if (a.part) all += y;
             else a.dg[(row0 + t) * a.H + h] = (float)y;

@@ -14,10 +14,14 @@
 // (a, b, c) = (q, k, v), (do, v, k), (v, do, q) and (k, q, do), the last two
 // from the last chunk to the first.  dg_t sums every pair i >= t > j, the
 // states before and the gradients behind; per chunk
-//   dg_t = <S', E> + sum_{i>=t} (qs_i + R_i - C_i - ks_i),
+//   dg_t = e^{G_last} <S, E> + sum_{i>=t} (qs_i + R_i - C_i) + sum_{j<t} ks_j,
 // qs_i = q_i times the state's part of dq_i, ks_i = k_i times that of dk_i,
 // R and C the row and column sums of the pairs (q_i k_j)(do_i v_j) e^{G_i-G_j},
-// j < i: sums of decayed terms only, so strong decays keep their digits.
+// j < i: sums of terms that a gate has decayed, so strong decays keep their digits.
+// In the chunks before a segment's last one E itself is decayed, and
+//   dg_t = <S', E> + sum_{i>=t} (qs_i + R_i - C_i - ks_i)
+// carries the sum on, <S', E> being dg of the next chunk's first token.  (In the last one
+// ks of the last token, k (dht v), has met no gate and would have to cancel.)
 //
 // A workgroup of four waves walks the chunks of one segment of one head.  Each
 // wave owns a quarter of the columns of c and S; S stays in MFMA accumulators,
@@ -176,6 +180,24 @@ struct DecayBody {
         return ((kt * CT + ct) * 4 + w) * 256 + lane * 4;
     }
 
+    // the wave's share of <S, E>, E in memory (nullptr: zeros)
+    __device__ __forceinline__ static void end_dot(const f32x4 (&S)[KT][CT], const float* e0, int w, int lane, Shared& s) {
+        float d = 0.f;
+        if (e0) {
+            asm volatile("" : "+v"(lane));   // (the addresses are made here)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane, kt, ct, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d += v[e] * S[kt][ct][e];
+                }
+        }
+        d = wave_sum(d);
+        if (lane == 0) s.ends[w] = d;
+    }
+
     // block: the workgroup's number among those of this walk
     __device__ static void run(const DecayWalk& p, unsigned block, Shared& s) {
         const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), g16 = lane >> 4, r16 = lane & 15;
@@ -284,6 +306,10 @@ struct DecayBody {
             }
         }
         float total = 1.f;   // LOCAL: decay of the segment
+        // DOT 2: the gradient behind the segment
+        const float* e0 = DOT != 2 ? nullptr
+                          : single ? (p.seq_end ? p.seq_end + (t.seq * p.H + h) * KV : nullptr)
+                                   : p.tile_end + (blk * p.H + h) * KV;
 
         if (nch > 0 && w == GW)
             make_gates<REV>(s.gates[0], gfirst, t.n - first_of(0), p.in_scale, p.up_scale, lane);
@@ -436,6 +462,9 @@ struct DecayBody {
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) S[kt][ct][e] *= dec;
+            if constexpr (DOT == 2) {       // what reaches the gradient behind the last chunk from before it
+                if (j + 1 == nch) end_dot(S, e0, w, lane, s);
+            }
 #pragma unroll
             for (int js = 0; js < 2; ++js) {
                 frag cp[CT][E8::PARTS];
@@ -568,24 +597,9 @@ struct DecayBody {
                 }
         }
         if (LOCAL && tid == 0) p.dec[blk * p.H + h] = total;
-        if constexpr (DOT == 2) {      // <S', E> at the segment's end
-            const float* e0 = single ? (p.seq_end ? p.seq_end + (t.seq * p.H + h) * KV : nullptr)
-                                     : p.tile_end + (blk * p.H + h) * KV;
-            float d = 0.f;
-            if (e0) {
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const f32x4 v = *reinterpret_cast<const f32x4*>(e0 + state_at(w, lane2, kt, ct, 0));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) d += v[e] * S[kt][ct][e];
-                    }
-            }
-            d = wave_sum(d);
-            if (lane == 0) s.ends[w] = d;
+        if constexpr (DOT == 2) {
             __syncthreads();
-            if (tid == 0) {
+            if (tid == 0 && nch > 0) {
                 float all = 0.f;
                 for (int i = 0; i < W; ++i) all += s.ends[i];
                 p.ends[blk * p.H + h] = all;

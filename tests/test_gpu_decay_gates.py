@@ -33,3 +33,18 @@ def test_gates_that_are_not_finite(gpu_lib, dt, bad, T, at):
         assert not bool(torch.isfinite(got[n][hit]).any()), n
     for n in ("ht", "dh0"):
         assert not bool(torch.isfinite(got[n][1, 1]).any()), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,HV,K,V", [(1, 1, 64, 64), (60, 1, 64, 64), (64, 2, 128, 64), (330, 1, 64, 64), (330, 2, 128, 128)])
+def test_strong_gates_and_a_final_gradient(gpu_lib, dt, T, HV, K, V):
+    """The final state's gradient meets the last token's k v^T undecayed, in no token's dg: 150 times the terms
+    that dg has.  Its relative error is 32-bit all the same: K products with V terms, 64 pairs, a chunk each."""
+    d = inputs(22, 2, T, 1, HV, K, V, dt)
+    d["g"] = -5 - torch.rand(2, T, HV, generator=torch.Generator().manual_seed(3))
+    c = {n: t.cuda() for n, t in d.items()}
+    got = gpu_lib.decay_attn_bwd(c["q"], c["k"], c["v"], c["g"], c["do"], h0=c["h0"], dht=c["dht"])["dg"].cpu().double()
+    torch.cuda.synchronize()
+    want = ref.decay(d["q"], d["k"], d["v"], d["g"], None, d["h0"], None, d["do"], d["dht"])[0]["dg"]
+    e = (got - want).norm() / want.norm()
+    assert e <= (K + V + 64 + -(-T // 64)) * 2.0 ** -24, float(e)
