@@ -129,18 +129,24 @@ struct alignas(16) ChunkGates {
     float hi[64], lo[64], in[64], out[64];
     float dec;
 };
+// Token of the chunk whose gate a lane brings: reversed walks sum from the end, so that a gate that is
+// not finite stays out of the sums behind it.
+template <bool REV> __device__ __forceinline__ int gate_token(int lane) { return REV ? 63 - lane : lane; }
 template <bool REV>
 __device__ __forceinline__ void make_gates(ChunkGates& s, float g, int n, float in_scale, float up_scale, int lane) {
-    const bool on = lane < n;
-    const GateParts p = gate_parts(on ? g : 0.f);
-    const float ph = scan64(p.hi), pl = scan64(p.lo), th = lane_of(ph, 63), tl = lane_of(pl, 63);
-    // (from behind a sum of its own, not what is left of the whole: a gate that is not finite
-    // may not reach the tokens behind it)
-    const float hi = REV ? behind64(p.hi, lane) : ph, lo = REV ? behind64(p.lo, lane) : pl;
-    s.hi[lane] = on ? hi : REV ? 8192.f * 64 : -8192.f * 64;
-    s.lo[lane] = lo;
-    s.in[lane] = on ? in_scale * exp2_hw(hi + lo) : 0.f;
-    s.out[lane] = on ? up_scale * (REV ? exp2_hw(ph + pl) : exp2_hw((th - hi) + (tl - lo))) : 0.f;
+    const GateParts p = gate_parts(gate_token<REV>(lane) < n ? g : 0.f);
+    float hi = scan64(p.hi), lo = scan64(p.lo);
+    const float th = lane_of(hi, 63), tl = lane_of(lo, 63);
+    int at = lane;
+    if (REV) {     // a lane has the sum from its token on, which is the one behind the token before it
+        at = lane < 63 ? 62 - lane : 63;
+        if (lane == 63) hi = lo = 0.f;
+    }
+    const bool on = at < n;
+    s.hi[at] = on ? hi : REV ? 8192.f * 64 : -8192.f * 64;
+    s.lo[at] = lo;
+    s.in[at] = on ? in_scale * exp2_hw(hi + lo) : 0.f;
+    s.out[at] = on ? up_scale * exp2_hw((th - hi) + (tl - lo)) : 0.f;
     if (lane == 0) s.dec = exp2_hw(th + tl);
 }
 
@@ -180,8 +186,9 @@ struct DecayBody {
         return ((kt * CT + ct) * 4 + w) * 256 + lane * 4;
     }
 
-    // the wave's share of <S, E>, E in memory (nullptr: zeros)
-    __device__ __forceinline__ static void end_dot(const f32x4 (&S)[KT][CT], const float* e0, int w, int lane, Shared& s) {
+    // the wave's share of dec <S, E>, E in memory (nullptr: zeros)
+    __device__ __forceinline__ static void end_dot(const f32x4 (&S)[KT][CT], const float* e0, float dec, int w, int lane,
+                                                   Shared& s) {
         float d = 0.f;
         if (e0) {
             asm volatile("" : "+v"(lane));   // (the addresses are made here)
@@ -195,7 +202,7 @@ struct DecayBody {
                 }
         }
         d = wave_sum(d);
-        if (lane == 0) s.ends[w] = d;
+        if (lane == 0) s.ends[w] = dec * d;
     }
 
     // block: the workgroup's number among those of this walk
@@ -248,7 +255,7 @@ struct DecayBody {
             if (DOT) nx.load(px + t0 * p.x.ts, (unsigned)p.x.ts, n, tid);
         };
         const auto gate_of = [&](int j) {
-            const int at = min(first_of(j) + lane, t.n - 1);
+            const int at = min(first_of(j) + gate_token<REV>(lane), t.n - 1);
             return pg[at * p.gs];
         };
 
@@ -323,6 +330,10 @@ struct DecayBody {
             if (w == GW && j + 1 < nch) {
                 make_gates<REV>(s.gates[(j + 1) & 1], gnext, t.n - first_of(j + 1), p.in_scale, p.up_scale, lane);
                 if (j + 2 < nch) gnext = gate_of(j + 2);
+            }
+
+            if constexpr (DOT == 2) {   // what reaches the gradient behind the last chunk from before it
+                if (j + 1 == nch) end_dot(S, e0, gt.dec, w, lane, s);
             }
 
             // What the others wait for at the next barrier goes before the other workgroup's products
@@ -462,9 +473,6 @@ struct DecayBody {
                 for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) S[kt][ct][e] *= dec;
-            if constexpr (DOT == 2) {       // what reaches the gradient behind the last chunk from before it
-                if (j + 1 == nch) end_dot(S, e0, w, lane, s);
-            }
 #pragma unroll
             for (int js = 0; js < 2; ++js) {
                 frag cp[CT][E8::PARTS];
