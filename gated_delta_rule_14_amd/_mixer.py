@@ -223,18 +223,20 @@ def _pages(k_cache, v_cache, page_table, lens, like, heads, D, dev):
     return _pages_plan(N, M, sh[0], sh[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), N
 
 
-def _look(k_cache, page_table, lens, T, cu_seqlens, stream, dev):
-    """With GDN_DEBUG set: raise where a position in use has no page, T tokens (or a packed
-    sequence's) after lens."""
+def _look(k_cache, page_table, lens, stream, dev, T=None, cu_seqlens=None, window=0):
+    """With GDN_DEBUG set: raise where a position in use has no page: T tokens (or a packed
+    sequence's) from lens on, or without T the last `window` before lens (0: all)."""
     if not _debug():
         return
     (stream or torch.cuda.current_stream(dev)).synchronize()
-    table, n = page_table.cpu(), lens.cpu()
-    end = n + (T if cu_seqlens is None else (cu_seqlens[1:] - cu_seqlens[:-1]).cpu())
-    cap = table.shape[1] * k_cache.shape[1]
-    if bool(((n < 0) | (end > cap)).any()):
+    table, n, P = page_table.cpu(), lens.cpu(), k_cache.shape[1]
+    cap = table.shape[1] * P
+    new = 0 if T is None else T if cu_seqlens is None else (cu_seqlens[1:] - cu_seqlens[:-1]).cpu()
+    if bool(((n < 0) | (n + new > cap)).any()):
         raise ValueError("lens must be in 0 .. %d with the new tokens" % cap)
-    used = torch.arange(table.shape[1])[None] * k_cache.shape[1] < end[:, None]
+    first, end = (n, n + new) if T is not None else ((n - window).clamp(min=0) if window > 0 else 0 * n, n)
+    at = torch.arange(table.shape[1])[None] * P
+    used = (at < end[:, None]) & (at + P > first[:, None]) & (first < end)[:, None]
     if bool((used & ((table < 0) | (table >= k_cache.shape[0]))).any()):
         raise ValueError("page_table holds a page outside the cache")
 
@@ -289,7 +291,7 @@ def paged_append(q, k, v, k_cache, v_cache, page_table, lens, inv_freq=None, pos
     else:
         with _on(stream):   # allocated on the kernel's stream (see chunk_fwd)
             q_out = _like(q)
-    _look(k_cache, page_table, lens, T, cu_seqlens, stream, dev)
+    _look(k_cache, page_table, lens, stream, dev, T=T, cu_seqlens=cu_seqlens)
     _run(lib.gdn_paged_append, dev, stream, p.at, c.at, _p(q), k.data_ptr(), v.data_ptr(), vt, vh, _p(q_weight),
          _p(k_weight), _p(inv_freq), _p(positions), _p(cu_seqlens), page_table.data_ptr(), lens.data_ptr(), _p(q_out),
          k_cache.data_ptr(), v_cache.data_ptr())
@@ -333,7 +335,7 @@ def paged_attn(q, k_cache, v_cache, page_table, lens, scale=None, window=0, o=No
         if o is None:
             o = _like(q)
         workspace, have = _workspace(workspace, p.fwd, dev, q)
-    _look(k_cache, page_table, lens, 0, None, stream, dev)
+    _look(k_cache, page_table, lens, stream, dev, window=int(window))
     _run(lib.gdn_paged_attn, dev, stream, p.at, c.at, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
          page_table.data_ptr(), lens.data_ptr(), o.data_ptr(), _p(workspace), have)
     return o
