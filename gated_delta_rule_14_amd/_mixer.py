@@ -232,7 +232,7 @@ def _look(k_cache, page_table, lens, stream, dev, T=None, cu_seqlens=None, windo
     table, n, P = page_table.cpu(), lens.cpu(), k_cache.shape[1]
     cap = table.shape[1] * P
     new = 0 if T is None else T if cu_seqlens is None else (cu_seqlens[1:] - cu_seqlens[:-1]).cpu()
-    if bool(((n < 0) | (n + new > cap)).any()):
+    if bool(((n < 0) | (n > cap) | (n + new > cap)).any()):
         raise ValueError("lens must be in 0 .. %d with the new tokens" % cap)
     first, end = (n, n + new) if T is not None else ((n - window).clamp(min=0) if window > 0 else 0 * n, n)
     at = torch.arange(table.shape[1])[None] * P

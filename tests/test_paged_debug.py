@@ -48,7 +48,7 @@ def test_pages_that_an_append_does_not_write_may_be_gone():
             look(table, lens, T=16)
 
 
-@pytest.mark.parametrize("n", [-1, 49, -MAX])
+@pytest.mark.parametrize("n", [-1, 49, MAX, MAX - 3, -MAX])
 def test_lengths_outside_the_table(n):
     for kw in (dict(T=4), dict(T=0), dict(window=0), dict(window=5), dict(cu_seqlens=torch.tensor([0, 4]), T=4)):
         with pytest.raises(ValueError, match="lens"):
