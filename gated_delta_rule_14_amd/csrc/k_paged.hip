@@ -135,6 +135,16 @@ hipError_t launch_paged_append(const PagedAppend& a) {
 // 4.4 TB/s.  One request of 1000 tokens: 8 us, the look-ups of length and page, three
 // turns of loads and the meeting of the waves, and 4 us for the join.
 constexpr int UNIT = 128;       // tokens that a piece is a multiple of
+constexpr int MOST = 1 << 23;   // units of a sequence at most (a table's row is below 2^30 tokens)
+
+// Units of a piece where all sequences together have `all`.  No piece needs more than a sequence has; the
+// quotient alone passes 31 bits with 2048 key heads (one piece) and 256 rows of 2^30 tokens that share pages.
+constexpr int piece_units(int64_t all, int64_t share) {
+    const int64_t per = (all + share - 1) / share;
+    return per < 1 ? 1 : per > MOST ? MOST : (int)per;
+}
+static_assert(piece_units(0, 7) == 1 && piece_units(8, 7) == 2 && piece_units(14, 7) == 2, "rounded up");
+static_assert(piece_units((int64_t)512 << 23, 1) == MOST && piece_units((int64_t)1 << 54, 1) == MOST, "in 31 bits");
 
 struct Piece {
     int64_t n;                  // sequence; < 0: none
@@ -165,7 +175,7 @@ __device__ __forceinline__ Piece find_piece(const PagedAttn& a, int64_t at, int6
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off, 64);
-    const int per = (int)max((int64_t)1, (all + a.share - 1) / a.share);
+    const int per = piece_units(all, a.share);
     Piece p;
     p.n = -1;
     int64_t before = 0;
