@@ -251,9 +251,9 @@ def paged_append(q, k, v, k_cache, v_cache, page_table, lens, inv_freq=None, pos
     int64 (not changed).  Sequence n is batch row n, or with cu_seqlens [N + 1]
     the n-th packed one.  `positions` [B, T] int64 for the rotation (None:
     lens[n] + t).  q [B, T, Hq, D] is normed and rotated alike; returns it
-    (None for q None).  With GDN_DEBUG set, lengths and pages are looked at
-    and a ValueError raised for those outside the cache, which are otherwise
-    left out."""
+    (None for q None).  With GDN_DEBUG set, lengths and the pages of the
+    positions written are looked at and a ValueError raised for those outside
+    the cache, which are otherwise left out."""
     lib = _b.load()
     dev, ks = _device(k, "k"), k.shape
     if len(ks) != 4 or v.shape != ks:
@@ -325,8 +325,8 @@ def paged_attn(q, k_cache, v_cache, page_table, lens, scale=None, window=0, o=No
     their cached tokens (see paged_append), Hq a multiple of Hk.  lens [N]
     int64 counts the new token too where its key is to be seen.  scale
     defaults to D^-0.5.  Returns o [N, Hq, D]; zeros where lens is 0.  With
-    GDN_DEBUG set, lengths and pages outside the cache raise a ValueError;
-    they are otherwise left out."""
+    GDN_DEBUG set, lengths and pages (of the positions attended to) outside
+    the cache raise a ValueError; they are otherwise left out."""
     lib = _b.load()
     p, c, dev = _attn(q, k_cache, v_cache, page_table, lens, scale, window)
     if o is not None:

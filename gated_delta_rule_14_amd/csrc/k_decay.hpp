@@ -34,16 +34,19 @@
 // What bounds it: two workgroups fill a compute unit's registers and LDS, two
 // waves to a SIMD, which take turns at the matrix unit, the vector ALU and LDS
 // (of 64 tokens of a head the output walk has 150 matrix and 600 vector
-// instructions a wave).  16 heads of 128 x 128 in bf16, 16384 tokens: segments'
-// states 35 us (134 MB read, 3.8 TB/s), output 66 us (268 MB, 4.1 TB/s; 70 where it
-// chains the states of eight segments as well), the three gradient walks together
-// 250 us, the matrix unit busy for a quarter of it, the vector ALU and LDS for about
-// two fifths each.  Eight waves of 16 columns each: 76 us for the output instead of 68, each
+// instructions a wave).  16 heads of 128 x 128 in bf16, 16384 tokens, medians of a
+// trace: segments' states 38 us (134 MB read, 3.5 TB/s), output 71 us (268 MB,
+// 3.8 TB/s; with the chaining of the states of eight segments), the three gradient walks
+// together 257 us, the matrix unit busy for a quarter of it, the vector ALU and LDS for
+// about two fifths each.  Eight waves of 16 columns each: 76 us for the output instead of 68, each
 // then reads all of a and b for half as many products.
 //
 // Roundings: products are of the inputs' type, sums in 32 bits.  With bf16 the
 // pairs' weights and the state are rounded to bf16 where they are multiplied
-// into an output of that type (each as much as the output's own rounding); where
+// into an output of that type.  Each is a rounding of factors of many terms, the two
+// together as much as the output's own: o's error is 0.0023 of its norm, where its
+// rounding alone makes 0.0017 (4 x 4096 tokens of 16 heads of 128); a second part would
+// double the state's and the pairs' products.  Where
 // a 32-bit result depends on them (the state itself, dg) the factor is split into
 // three bf16 parts, 24 bits, and multiplied part by part.
 #pragma once
@@ -78,9 +81,9 @@ template <typename T, int D, int NT> struct Ahead {
     }
 };
 
-// Gates of a chunk in log2, as a multiple of 1/16 and a rest of up to 1/32, whose
-// running sums are exact and below 2 (the sum of the gates themselves would lose
-// the small ones behind a large one).  A gate below -150 (2^-150 is 0 in 32 bits)
+// Gates of a chunk in log2, as a multiple of 1/16 and a rest of up to 1/32.  Running
+// sums of the multiples are exact; those of the rests, below 2, are off by a few 2^-24
+// (the sum of the gates themselves would lose the small ones behind a large one).  A gate below -150 (2^-150 is 0 in 32 bits)
 // counts as -8192, whose power and every sum with it is 0: nothing passes it.
 struct GateParts {
     float hi, lo;

@@ -4,8 +4,8 @@
 // They need nothing of each other, so one launch runs all three, the workgroups of
 // a segment's head next to each other on one XCD: dk and dv read the same rows at
 // about the same time, and no walk's end leaves the chip half idle (2 x 8192 tokens
-// of 16 heads of 128: 250 us, as three launches 262; 300 tokens of 4 heads, the whole
-// backward 64 -> 36 us).
+// of 16 heads of 128: 257 us, as three launches 12 us more; 300 tokens of 4 heads, the
+// whole backward 29 us, as three launches and with longer segments 64).
 #include "k_decay.hpp"
 
 namespace gdn {

@@ -128,7 +128,8 @@ hipError_t launch_paged_append(const PagedAppend& a) {
 // Scores are K Q^T, tokens in the accumulator's rows, so they are at once the
 // operand of the output's product V^T P^T, whose V^T comes out of LDS by
 // transposing reads.  With bf16 the weights go into that product in two parts,
-// 16 bits.
+// 16 bits, whose error of 2^-16 is lost in the output's rounding of 2^-8 (in one part it
+// would be as large); the sum that divides them keeps 32.
 //
 // Bound by HBM: 16 requests of 20000 to 65536 tokens (3.0 GB of keys and values,
 // 8 heads of 128) 545 us, 5.5 TB/s; 64 of 1 to 8192 (2 heads of 256) 146 us,
